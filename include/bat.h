@@ -313,6 +313,107 @@ BAT_API bat_status_t bat_kv_dequantize(const void* cache_codes, const void* cach
                                        const float* A, int shared, const float* B, void* out,
                                        bat_out_dtype_t out_dtype, void* stream);
 
+/* One K (or V) cache of num_slots rows, laid out as bat_kv_quantize writes it. */
+typedef struct {
+  const void* codes;  /* device, bat_kv_codes_bytes(num_slots, H, D, fmt) bytes, 16-byte aligned */
+  const void* scales; /* device, bat_kv_scales_bytes(num_slots, H, D) bytes */
+  int64_t num_slots;
+  int64_t H;          /* KV heads */
+  int64_t D;          /* head_dim */
+  bat_kv_format_t fmt;
+} bat_kv_cache_t;
+
+/*
+ * Attention of a batch's new tokens over the paged quantized cache (the BATQuant note,
+ * Key Designs 4: the K and V paths' transform sets; scores and softmax stay in high
+ * precision). The new tokens' K and V are stored first (bat_kv_quantize), then this call
+ * lets every new token attend over its sequence's cache rows:
+ *
+ *   sequence b has the new tokens q_starts[b] .. q_starts[b+1] - 1 (n_b of them, 0 allowed)
+ *   and kv_lens[b] cached tokens, the new ones last; cached token j is cache slot
+ *   page_table[b][j / page_size] * page_size + j % page_size.
+ *   New token i of sequence b is at position p = kv_lens[b] - n_b + i and sees
+ *     0 <= j <= p  and  (window == 0  or  j > p - window  or  j < sinks).
+ *   head h attends with KV head h / (Hq / H):
+ *     s_j = scale * (q P_q) . k_j,   out = (sum_j softmax(s)_j v_j) P_o,
+ *   k_j, v_j the stored values (code times 2^(scale byte - 127)), P_q and P_o
+ *   block-diagonal with B_b (x) A per 32 channels, the same for all heads: with the K path
+ *   stored through P_k and the V path through P_v, P_q = P_k^-T and P_o = P_v^-1 give the
+ *   attention of the untransformed K and V.
+ *
+ *   q        : bf16, token t and head h at q + t * q_stride + h * D (q_stride in elements,
+ *              >= Hq * D, a multiple of 8: a slice of a fused qkv output needs no copy);
+ *              16-byte aligned; [T][Hq][D].
+ *   K, V     : the caches; same num_slots, H, D and fmt. Hq must be a multiple of H.
+ *   page_table : device int32 [B][max_pages]. Only entries of tokens that some row sees are
+ *              read; one that points outside the cache hides its tokens and sets the device
+ *              error word (bat_device_error).
+ *   kv_lens  : device int32 [B]; q_starts: device int32 [B + 1], ascending. Both are read on
+ *              the device, at the time the kernels run: a captured call may be replayed with
+ *              other values. A length over max_pages * page_size (or 2^30, or below 0) and
+ *              a start outside [0, T] are clamped and set the device error word.
+ *   max_q_len: the largest n_b that the call may meet (host value; it picks the kernel and
+ *              the workspace's size; results are right for longer chunks too).
+ *   scale    : finite; usually 1 / sqrt(D).
+ *   window   : 0 for none, else >= 1; sinks >= 0 (first tokens that stay visible behind the
+ *              window; without a window they change nothing).
+ *   Aq, q_shared, Bq / Ao, o_shared, Bo : factors of P_q / P_o as in bat_quantize_act_gpk
+ *              (device fp32 [s][s] and [D/32][32/s][32/s]), or both NULL for none.
+ *   out      : bf16 [T][Hq][D] contiguous, 16-byte aligned. A row that sees nothing gives 0.
+ *              Tokens behind q_starts[B] are left as they were.
+ *   lse      : fp32 [T][Hq] or NULL: ln sum_j exp(s_j); -inf for a row that sees nothing.
+ *   workspace: device, >= bat_kv_attention_workspace_bytes(...) bytes, 256-byte aligned,
+ *              its contents unused after the call. Calls that may overlap on the GPU need
+ *              one each.
+ * Arithmetic: stored values are used exactly (scales up to 2^39 for KV8, 2^33 for KV4; a larger
+ * one, a scale byte 255 or an E4M3 NaN counts as NaN for the rows that see it; products of a
+ * weight and a value below 2^-94 may count as 0). q P_q is rounded to bf16 and the softmax weights
+ * to bf16 for the products; scores, maxima, sums and outputs are held in fp32 and out is
+ * rounded once. Sums run in a fixed order: results do not depend on timing.
+ * Errors: BAT_ERR_UNSUPPORTED (a factor split, or K->fmt != V->fmt), BAT_ERR_INVALID_ARG
+ * (null pointers, sizes < 1, one factor of a pair only, scale not finite, window or sinks
+ * < 0), BAT_ERR_SHAPE (D % 32, D > 256, Hq % H, caches that differ, q_stride, more than 2^30
+ * rows or T * Hq), BAT_ERR_ALIGN, BAT_ERR_WORKSPACE, BAT_ERR_CUDA.
+ */
+BAT_API size_t bat_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D,
+                                                int64_t max_q_len, int has_q_factors);
+BAT_API bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride,
+                                      const bat_kv_cache_t* K, const bat_kv_cache_t* V,
+                                      const int32_t* page_table, int64_t B, int64_t max_pages,
+                                      int64_t page_size, const int32_t* kv_lens,
+                                      const int32_t* q_starts, int64_t max_q_len, float scale,
+                                      int64_t window, int64_t sinks, const float* Aq, int q_shared,
+                                      const float* Bq, const float* Ao, int o_shared,
+                                      const float* Bo, void* out, float* lse, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * RMS norm of the residual stream into the quantizer, the step before a quantized linear
+ * layer: h = X + residual, y = h / sqrt(mean_k(h^2) + eps) * weight, then the transform and
+ * clip of bat_quantize_act_gpk and MXFP4 or MXFP8 quantization of y (formats and scale rule
+ * of bat_quantize_act / bat_quantize_act_mxfp8). h and y are fp32; nothing is rounded
+ * between the inputs and the codes.
+ *   X        : bf16 [M][K]; residual: bf16 [M][K] or NULL (h = X).
+ *   weight   : bf16 [K].
+ *   eps      : finite, >= 0.
+ *   A, shared, B : factors as in bat_quantize_act_gpk, or both NULL for no transform
+ *              (shared is then unused); g_lo, g_hi: [K/32] clip logits, or both NULL.
+ *   fmt      : BAT_KV_MXFP8 (Xq is a bat_mxfp8_t) or BAT_KV_MXFP4 (a bat_mxfp4_t).
+ *   Xq       : output, Xq->rows == M, Xq->k == K, ready for bat_w4a8_gemm / bat_mxfp4_gemm.
+ *   residual_out : bf16 [M][K] or NULL: h rounded to bf16, the new residual stream. May be
+ *              `residual` itself or X itself; other overlaps are not allowed.
+ *   y_out    : optional fp32 [M][K] trace of the transformed values (NULL to skip).
+ * All pointers 16-byte aligned (g_lo, g_hi: 4). Errors: BAT_ERR_UNSUPPORTED (the split),
+ * BAT_ERR_INVALID_ARG (null pointers, one of a pair only, M < 1, K < 32, eps, fmt),
+ * BAT_ERR_SHAPE, BAT_ERR_ALIGN, BAT_ERR_CUDA, as in bat_quantize_act_gpk.
+ */
+BAT_API bat_status_t bat_rmsnorm_quantize(const void* X, const void* residual, const void* weight,
+                                          int64_t M, int64_t K, float eps, const float* A,
+                                          int shared, const float* B, const float* g_lo,
+                                          const float* g_hi, bat_kv_format_t fmt,
+                                          const bat_mxfp4_t* Xq, void* residual_out, float* y_out,
+                                          void* stream);
+
 /*
  * Block-scaled MXFP4 GEMM on the 5th-generation tensor cores (tcgen05,
  * kind::mxf4, fp32 accumulation in tensor memory):

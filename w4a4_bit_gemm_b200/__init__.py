@@ -41,6 +41,12 @@ class MXFP4Struct(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("k", ctypes.c_int64)]
 
 
+class KVCacheStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("num_slots", ctypes.c_int64), ("H", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("fmt", ctypes.c_int)]
+
+
 _lib = None
 
 
@@ -53,7 +59,8 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(f"{LIB_PATH} is missing: run w4a4_bit_gemm_b200.build.build() first")
     L = ctypes.CDLL(LIB_PATH)
     P, I64, S = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
-    SP = ctypes.POINTER(MXFP4Struct)
+    SP, KP = ctypes.POINTER(MXFP4Struct), ctypes.POINTER(KVCacheStruct)
+    F, Z = ctypes.c_float, ctypes.c_size_t
     sig = {
         "bat_mxfp4_codes_bytes": (ctypes.c_size_t, [I64, I64]),
         "bat_mxfp4_scales_bytes": (ctypes.c_size_t, [I64, I64]),
@@ -75,6 +82,10 @@ def lib() -> ctypes.CDLL:
         "bat_kv_scales_bytes": (ctypes.c_size_t, [I64, I64, I64]),
         "bat_kv_quantize": (S, [P, I64, I64, I64, P, S, P, P, P, P, S, P, P, I64, P, P]),
         "bat_kv_dequantize": (S, [P, P, I64, I64, I64, S, P, I64, P, S, P, P, S, P]),
+        "bat_kv_attention_workspace_bytes": (Z, [I64, I64, I64, I64, I64, S]),
+        "bat_kv_attention": (S, [P, I64, I64, I64, KP, KP, P, I64, I64, I64, P, P, I64, F, I64, I64,
+                                 P, S, P, P, S, P, P, P, P, Z, P]),
+        "bat_rmsnorm_quantize": (S, [P, P, P, I64, I64, F, P, S, P, P, P, S, SP, P, P, P]),
         "bat_selftest_bounded_wait": (S, [ctypes.c_uint64, P, P]),
         "bat_mxfp4_gemm": (S, [SP, SP, P, S, P]),
         "bat_linear_workspace_bytes": (ctypes.c_size_t, [I64, I64]),
@@ -517,6 +528,10 @@ class KVCache:
         return KVCache(torch.zeros(cb, dtype=torch.uint8, device=device),
                        torch.zeros(sb, dtype=torch.uint8, device=device), num_slots, H, D, fmt)
 
+    def struct(self) -> KVCacheStruct:
+        return KVCacheStruct(self.codes.data_ptr(), self.scales.data_ptr(), self.num_slots, self.H,
+                             self.D, _KV_FMT[self.fmt])
+
     def check(self, device) -> "KVCache":
         """Both buffers on `device` and large enough for num_slots x H x D (before any launch)."""
         if self.fmt not in _KV_FMT:
@@ -571,6 +586,139 @@ def bat_kv_dequantize(cache: KVCache, slots, A=None, B=None, out: Optional[torch
                                    cache.D, _KV_FMT[cache.fmt], _ptr(slots), T, _ptr(A), s, _ptr(B),
                                    _ptr(out), code, _stream(stream)), "bat_kv_dequantize")
     return out
+
+
+def bat_kv_attention_workspace_bytes(T: int, Hq: int, H: int, D: int, max_q_len: int,
+                                     has_q_factors: bool = False) -> int:
+    return lib().bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len, 1 if has_q_factors else 0)
+
+
+def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
+    """A workspace of this call alone, in the allocator's order on the stream that uses it."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+
+
+def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q_starts, page_size: int,
+                     max_q_len: int, scale: Optional[float] = None, window: int = 0, sinks: int = 0,
+                     q_factors=None, out_factors=None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """Attention of new tokens q [T][Hq][D] (bf16) over the paged caches; returns out [T][Hq][D].
+
+    Sequence b has tokens q_starts[b]:q_starts[b+1] of q and kv_lens[b] cached tokens (its new
+    ones last, already stored); token j lies in cache slot page_table[b, j // page_size] *
+    page_size + j % page_size. Causal, with an optional sliding window and ``sinks`` first
+    tokens that stay visible. ``q_factors`` / ``out_factors`` = (A, B): block transforms of q
+    and of the output. ``lse`` (fp32 [T][Hq]) receives the log of the softmax sums. q may be
+    a slice of a wider row (its token stride is free, heads and channels are contiguous).
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [T][Hq][D]")
+    T, Hq, D = q.shape
+    dev = q.device
+    if dev.type != _DEVICE_TYPE:
+        raise ValueError("q must be a CUDA tensor")
+    if q.dtype != torch.bfloat16:
+        raise ValueError(f"q must be torch.bfloat16, got {q.dtype}")
+    s0, s1, s2 = q.stride()
+    if s2 != 1 or (s1 != D and Hq > 1):
+        raise ValueError("q's heads and channels must be contiguous (only the token stride is free)")
+    q_stride = s0 if T > 1 else max(s0, Hq * D)
+    if kcache.D != D or vcache.D != D or kcache.H != vcache.H or kcache.num_slots != vcache.num_slots:
+        raise ValueError("the caches' shapes do not match each other and q")
+    kcache.check(dev)
+    vcache.check(dev)
+    _need(page_table, torch.int32, "page_table", None, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be two-dimensional")
+    B, max_pages = page_table.shape
+    _need(kv_lens, torch.int32, "kv_lens", (B,), dev)
+    _need(q_starts, torch.int32, "q_starts", (B + 1,), dev)
+    Aq = Bq = Ao = Bo = None
+    sq = so = 8
+    if q_factors is not None:
+        Aq, Bq = q_factors
+        sq = _gpk_factors(Aq, Bq, D, dev)
+    if out_factors is not None:
+        Ao, Bo = out_factors
+        so = _gpk_factors(Ao, Bo, D, dev)
+    if lse is not None:
+        _need(lse, torch.float32, "lse", (T, Hq), dev)
+    _on_device(dev, stream)
+    need = bat_kv_attention_workspace_bytes(T, Hq, kcache.H, D, max_q_len, Aq is not None)
+    if workspace is None:
+        workspace = _scratch(need, dev, stream)
+    _need(workspace, torch.uint8, "workspace", None, dev)
+    if out is None:
+        if stream is None:
+            out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    _need(out, torch.bfloat16, "out", (T, Hq, D), dev)
+    k, v = kcache.struct(), vcache.struct()
+    _check(lib().bat_kv_attention(_ptr(q), T, Hq, q_stride, ctypes.byref(k), ctypes.byref(v),
+                                  _ptr(page_table), B, max_pages, page_size, _ptr(kv_lens),
+                                  _ptr(q_starts), max_q_len, D ** -0.5 if scale is None else scale,
+                                  window, sinks, _ptr(Aq), sq, _ptr(Bq), _ptr(Ao), so, _ptr(Bo),
+                                  _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)), "bat_kv_attention")
+    return out
+
+
+# ---------------------------------------------------------------- norm into the quantizer
+def bat_rmsnorm_quantize(X, weight, A=None, B=None, g_lo=None, g_hi=None,
+                         residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                         fmt: str = "mxfp8", Xq=None, residual_out: Optional[torch.Tensor] = None,
+                         y_out: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm of X + residual into the quantizer: returns (Xq, new residual or None).
+
+    h = X + residual; y = h / sqrt(mean(h^2) + eps) * weight; Xq = MX codes of y transformed
+    (A, B of any split; None: not) and clipped. The new residual stream (h in bf16) goes to
+    ``residual_out``, by default a new tensor when ``residual`` is given; it may be
+    ``residual`` (or X) itself.
+    """
+    _need(X, torch.bfloat16, "X")
+    if X.dim() != 2:
+        raise ValueError("X must be two-dimensional")
+    M, K = X.shape
+    dev = X.device
+    if fmt not in _KV_FMT:
+        raise ValueError(f"unknown format {fmt!r}")
+    _need(weight, torch.bfloat16, "weight", (K,), dev)
+    if (A is None) != (B is None):
+        raise ValueError("A and B must both be given or both be None")
+    s = 8 if A is None else _gpk_factors(A, B, K, dev)
+    _clip_args(g_lo, g_hi, K // 32, dev)
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual", (M, K), dev)
+    _on_device(dev, stream)
+    cls = MXFP8 if fmt == "mxfp8" else MXFP4
+    if stream is None:
+        Xq = cls.empty(M, K, dev) if Xq is None else Xq
+        if residual_out is None and residual is not None:
+            residual_out = torch.empty_like(residual)
+    else:
+        with torch.cuda.stream(stream):
+            Xq = cls.empty(M, K, dev) if Xq is None else Xq
+            if residual_out is None and residual is not None:
+                residual_out = torch.empty_like(residual)
+    if not isinstance(Xq, cls):
+        raise TypeError(f"Xq must be an {cls.__name__} for fmt {fmt!r}")
+    Xq.check("Xq", dev)
+    if residual_out is not None:
+        _need(residual_out, torch.bfloat16, "residual_out", (M, K), dev)
+    if y_out is not None:
+        _need(y_out, torch.float32, "y_out", (M, K), dev)
+    st = Xq.struct()
+    _check(lib().bat_rmsnorm_quantize(_ptr(X), _ptr(residual), _ptr(weight), M, K, eps, _ptr(A), s,
+                                      _ptr(B), _ptr(g_lo), _ptr(g_hi), _KV_FMT[fmt],
+                                      ctypes.byref(st), _ptr(residual_out), _ptr(y_out),
+                                      _stream(stream)), "bat_rmsnorm_quantize")
+    return Xq, residual_out
 
 
 def bat_selftest_bounded_wait(limit_ns: int = 50_000_000, stream=None) -> int:

@@ -13,11 +13,13 @@
 #include <vector>
 
 #include "../../include/bat.h"
+#include "bat_attn.cuh"
 #include "bat_common.cuh"
 #include "bat_gemm.cuh"
 #include "bat_gemm2.cuh"
 #include "bat_gemm_dec.cuh"
 #include "bat_kv.cuh"
+#include "bat_norm.cuh"
 #include "bat_prologue.cuh"
 
 namespace {
@@ -44,6 +46,7 @@ struct DeviceInfo {
   std::atomic<int> max_pairs{0};        // CTA pairs of that GEMM resident at once, 0 unknown
   std::atomic<int> dec_attr{0};         // the decode GEMM's smem attribute is set
   std::atomic<int> dec_clusters[9];     // [cluster size]: its clusters resident at once, 0 unknown
+  std::atomic<int> attn_attr{0};        // bit v: the attention kernel variant v has its smem attribute set
 };
 DeviceInfo g_dev[64];
 
@@ -648,6 +651,111 @@ bat_status_t check_gemm_args(const bat_mxfp4_t* Xq, const bat_mxfp4_t* Wq, const
 
 }  // namespace
 
+// ---------------------------------------------------------------- attention
+namespace {
+
+// CTAs that the chunks are dealt over: the workspace holds two partial results for each.
+constexpr int kAttnRowCtas = 296;
+
+// Row kernel: heads of a KV head that one unit takes.
+int attn_row_unit(int64_t G, int64_t D) { return G > 8 && D <= 128 ? 16 : 8; }
+
+size_t attn_part_bytes(int64_t ctas, int64_t rows, int64_t D) {
+  const size_t slots = static_cast<size_t>(2 * ctas) * static_cast<size_t>(rows);
+  return static_cast<size_t>(round_up(static_cast<int64_t>(slots * D * 4), 256) +
+                             round_up(static_cast<int64_t>(slots * 8), 256));
+}
+
+template <class Kernel>
+bat_status_t attn_smem(Kernel k, int dev, int bit, size_t max_bytes) {
+  const int m = 1 << bit;
+  if (!(g_dev[dev].attn_attr.load() & m)) {
+    const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(max_bytes));
+    if (e != cudaSuccess) return cuda_status(e);
+    g_dev[dev].attn_attr.fetch_or(m);
+  }
+  return BAT_OK;
+}
+
+template <class Kernel, class... Args>
+bat_status_t launch_dependent(Kernel k, dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, k, args...));
+}
+
+size_t attn_rows_smem(int nb4, int nt, int nb, bool qf, bool of) {
+  const size_t r = 8 * nt, dp = 128 * nb4;
+  size_t f = bat::attn::kWarps * r * (dp + 4) + bat::attn::kWarps * r * 2 + r * 2 + r * dp / 2;
+  if (qf || of) f += bat::kv::kFacFloats;
+  f += static_cast<size_t>(nb) * 1024 * ((qf ? 1 : 0) + (of ? 1 : 0));
+  return f * 4;
+}
+
+template <bool kFp8, int kNB4, int kNT>
+bat_status_t launch_attn_rows(bat::AttnParams& p, int dev, int sms, int bit, cudaStream_t s) {
+  auto k = bat::bat_attn_rows_kernel<kFp8, kNB4, kNT>;
+  const size_t smem = attn_rows_smem(kNB4, kNT, p.nb, p.qa != nullptr, p.oa != nullptr);
+  bat_status_t st = attn_smem(k, dev, bit, attn_rows_smem(kNB4, kNT, 4 * kNB4, true, true));
+  if (st != BAT_OK) return st;
+  // two CTAs an SM where registers and shared memory allow; a few chunks need fewer CTAs,
+  // but how many there are is known on the device only
+  const int per_sm = kNB4 == 1 && kNT == 1 && smem <= 110 * 1024 ? 2 : 1;
+  p.ctas = per_sm * sms < kAttnRowCtas ? per_sm * sms : kAttnRowCtas;
+  k<<<p.ctas, bat::attn::kThreads, smem, s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+template <int kTile>
+bat_status_t launch_attn_join(const bat::AttnParams& p, int dev, int bit, int ysplit, cudaStream_t s) {
+  if (p.ctas < 2) return BAT_OK;
+  auto k = bat::bat_attn_join_kernel<kTile>;
+  const size_t max_smem = (256 + 4 + bat::kv::kFacFloats + 8 * 1024) * 4;
+  const size_t smem = (p.D + 4 + (p.oa ? bat::kv::kFacFloats + p.nb * 1024 : 0)) * 4;
+  bat_status_t st = attn_smem(k, dev, bit, max_smem);
+  if (st != BAT_OK) return st;
+  return launch_dependent(k, dim3(p.ctas - 1, ysplit), dim3(256), smem, s, p);
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------- norm into the quantizer
+namespace {
+
+template <int kX, bool kFp8>
+bat_status_t launch_norm(const bat::NormParams& p, int sms, cudaStream_t s) {
+  const int nvec = p.K / 8;
+  // few rows: one vector a thread (latency); many rows: two or more, in smaller CTAs of
+  // which several share an SM (while one waits for its sum another loads)
+  int v = nvec <= 512 ? 1 : (nvec <= 1024 ? 2 : 4);
+  if (p.M > 2 * sms && nvec > 256 && nvec <= 512) v = 2;
+  if (kX == 2 && v > 1) v = nvec <= 512 ? 1 : 0;  // these splits' coefficients leave no registers for more
+  int nt = v > 1 ? static_cast<int>(round_up((nvec + v - 1) / v, 32)) : 0;
+  if (p.K > bat::norm::kMaxCachedK) v = 0;
+  if (v <= 1) nt = v == 0 ? bat::norm::kMaxThreads : static_cast<int>(round_up(nvec < 64 ? 64 : nvec, 32));
+  constexpr int kTwo = kX == 2 ? 0 : 2, kFour = kX == 2 ? 0 : 4;
+  void (*k)(bat::NormParams) = v == 1   ? bat::bat_rmsnorm_quantize_kernel<1, kX, kFp8>
+                               : v == 2 ? bat::bat_rmsnorm_quantize_kernel<kTwo, kX, kFp8>
+                               : v == 4 ? bat::bat_rmsnorm_quantize_kernel<kFour, kX, kFp8>
+                                        : bat::bat_rmsnorm_quantize_kernel<0, kX, kFp8>;
+  const int64_t cap = static_cast<int64_t>(sms) * (nt <= 256 ? 4 : 2);
+  const unsigned grid = static_cast<unsigned>(p.M < cap ? p.M : cap);
+  k<<<grid, nt, 0, s>>>(p);
+  return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
 extern "C" {
 
 int bat_version(void) { return 100; }
@@ -951,6 +1059,150 @@ bat_status_t bat_kv_dequantize(const void* cache_codes, const void* cache_scales
            : (f32 ? bat::bat_kv_dequantize_kernel<false, false, true> : bat::bat_kv_dequantize_kernel<false, false, false>);
   k<<<grid, bat::kv::kThreads, 0, s>>>(p);
   return cuda_status(cudaGetLastError());
+}
+
+size_t bat_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D,
+                                        int64_t max_q_len, int has_q_factors) {
+  if (T < 1 || Hq < 1 || H < 1 || Hq % H != 0 || D < 32 || D % 32 != 0 || D > 256 || max_q_len < 1) return 0;
+  (void)has_q_factors;
+  return attn_part_bytes(kAttnRowCtas, attn_row_unit(Hq / H, D), D);
+}
+
+bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride,
+                              const bat_kv_cache_t* K, const bat_kv_cache_t* V,
+                              const int32_t* page_table, int64_t B, int64_t max_pages,
+                              int64_t page_size, const int32_t* kv_lens, const int32_t* q_starts,
+                              int64_t max_q_len, float scale, int64_t window, int64_t sinks,
+                              const float* Aq, int q_shared, const float* Bq, const float* Ao,
+                              int o_shared, const float* Bo, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (!q || !K || !V || !page_table || !kv_lens || !q_starts || !out) return BAT_ERR_INVALID_ARG;
+  if (!K->codes || !K->scales || !V->codes || !V->scales) return BAT_ERR_INVALID_ARG;
+  if ((Aq == nullptr) != (Bq == nullptr) || (Ao == nullptr) != (Bo == nullptr)) return BAT_ERR_INVALID_ARG;
+  int qls = 3, ols = 3, cls = 0;
+  if (Aq && (qls = shared_log2(q_shared)) < 0) return BAT_ERR_UNSUPPORTED;
+  if (Ao && (ols = shared_log2(o_shared)) < 0) return BAT_ERR_UNSUPPORTED;
+  const int64_t H = K->H, D = K->D;
+  if (T < 1 || Hq < 1 || B < 1 || max_pages < 1 || page_size < 1 || max_q_len < 1 || window < 0 || sinks < 0 ||
+      !std::isfinite(scale))
+    return BAT_ERR_INVALID_ARG;
+  if (K->fmt != BAT_KV_MXFP8 && K->fmt != BAT_KV_MXFP4) return BAT_ERR_INVALID_ARG;
+  bat_status_t st = kv_shape_check(1, H, D, K->num_slots, 8, &cls);
+  if (st != BAT_OK) return st;
+  if (V->H != H || V->D != D || V->num_slots != K->num_slots) return BAT_ERR_SHAPE;
+  if (V->fmt != K->fmt) return BAT_ERR_UNSUPPORTED;
+  constexpr int64_t kMaxInt = 0x7FFFFFFF;
+  if (Hq % H != 0 || T > kMaxRows / Hq || q_stride < Hq * D || q_stride % 8 != 0 || B > kMaxRows ||
+      max_pages > kMaxInt || page_size > kMaxRows)
+    return BAT_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(K->codes) || !aligned16(V->codes) || !aligned16(out) ||
+      (Aq && (!aligned16(Aq) || !aligned16(Bq))) || (Ao && (!aligned16(Ao) || !aligned16(Bo))) ||
+      ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(kv_lens) |
+        reinterpret_cast<uintptr_t>(q_starts) | reinterpret_cast<uintptr_t>(lse)) & 3u) != 0)
+    return BAT_ERR_ALIGN;
+  const size_t need = bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len, Aq != nullptr);
+  if (!workspace || workspace_bytes < need) return BAT_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return BAT_ERR_ALIGN;
+  int dev = 0, sms = 0;
+  st = current_device(&dev, &sms);
+  if (st != BAT_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  bat::AttnParams p = {};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.k_codes = static_cast<const uint8_t*>(K->codes);
+  p.k_scales = static_cast<const uint8_t*>(K->scales);
+  p.v_codes = static_cast<const uint8_t*>(V->codes);
+  p.v_scales = static_cast<const uint8_t*>(V->scales);
+  p.table = page_table;
+  p.kv_lens = kv_lens;
+  p.q_starts = q_starts;
+  p.qa = Aq;
+  p.qb = Bq;
+  p.oa = Ao;
+  p.ob = Bo;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.T = T;
+  p.num_slots = K->num_slots;
+  p.capacity = max_pages > kMaxRows / page_size ? kMaxRows : max_pages * page_size;
+  p.B = static_cast<int>(B);
+  p.max_pages = static_cast<int>(max_pages);
+  p.page_size = static_cast<int>(page_size);
+  p.Hq = static_cast<int>(Hq);
+  p.Hkv = static_cast<int>(H);
+  p.G = static_cast<int>(Hq / H);
+  p.D = static_cast<int>(D);
+  p.nb = static_cast<int>(D / 32);
+  p.qls = qls;
+  p.ols = ols;
+  p.window = static_cast<int>(window < kMaxRows ? window : kMaxRows);
+  p.sinks = static_cast<int>(sinks < kMaxRows ? sinks : kMaxRows);
+  p.scale_log2 = scale * 1.4426950408889634f * bat::attn::kUp;
+  const bool fp8 = K->fmt == BAT_KV_MXFP8;
+  const int unit = attn_row_unit(p.G, D);
+  p.unit_rows = unit;
+  p.head_units = p.Hkv * ((p.G + unit - 1) / unit);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                       round_up(int64_t{2} * kAttnRowCtas * unit * D * 4, 256));
+  if (D > 128)
+    st = fp8 ? launch_attn_rows<true, 2, 1>(p, dev, sms, 0, s) : launch_attn_rows<false, 2, 1>(p, dev, sms, 1, s);
+  else if (unit == 16)
+    st = fp8 ? launch_attn_rows<true, 1, 2>(p, dev, sms, 2, s) : launch_attn_rows<false, 1, 2>(p, dev, sms, 3, s);
+  else
+    st = fp8 ? launch_attn_rows<true, 1, 1>(p, dev, sms, 4, s) : launch_attn_rows<false, 1, 1>(p, dev, sms, 5, s);
+  if (st != BAT_OK) return st;
+  return launch_attn_join<0>(p, dev, 6, unit, s);
+}
+
+bat_status_t bat_rmsnorm_quantize(const void* X, const void* residual, const void* weight, int64_t M,
+                                  int64_t K, float eps, const float* A, int shared, const float* B,
+                                  const float* g_lo, const float* g_hi, bat_kv_format_t fmt,
+                                  const bat_mxfp4_t* Xq, void* residual_out, float* y_out,
+                                  void* stream) {
+  if (!X || !weight || !Xq) return BAT_ERR_INVALID_ARG;
+  if ((A == nullptr) != (B == nullptr) || (g_lo == nullptr) != (g_hi == nullptr)) return BAT_ERR_INVALID_ARG;
+  int ls = 3;
+  if (A && (ls = shared_log2(shared)) < 0) return BAT_ERR_UNSUPPORTED;
+  if (fmt != BAT_KV_MXFP8 && fmt != BAT_KV_MXFP4) return BAT_ERR_INVALID_ARG;
+  if (M < 1 || K < 32 || !std::isfinite(eps) || eps < 0.0f) return BAT_ERR_INVALID_ARG;
+  if (K % 32 != 0 || K > kMaxK || M > kMaxRows) return BAT_ERR_SHAPE;
+  if (!aligned16(X) || (residual && !aligned16(residual)) || !aligned16(weight) ||
+      (A && (!aligned16(A) || !aligned16(B))) || (residual_out && !aligned16(residual_out)) ||
+      (y_out && !aligned16(y_out)) ||
+      ((reinterpret_cast<uintptr_t>(g_lo) | reinterpret_cast<uintptr_t>(g_hi)) & 3u) != 0)
+    return BAT_ERR_ALIGN;
+  bat_status_t st = check_mxfp4(Xq, M, K);
+  if (st != BAT_OK) return st;
+  int dev = 0, sms = 0;
+  st = current_device(&dev, &sms);
+  if (st != BAT_OK) return st;
+  bat::NormParams p = {};
+  p.x = static_cast<const uint16_t*>(X);
+  p.res = static_cast<const uint16_t*>(residual);
+  p.w = static_cast<const uint16_t*>(weight);
+  p.a = A;
+  p.b = B;
+  p.g_lo = g_lo;
+  p.g_hi = g_hi;
+  p.res_out = static_cast<uint16_t*>(residual_out);
+  p.codes = static_cast<uint8_t*>(Xq->codes);
+  p.scales = static_cast<uint8_t*>(Xq->scales);
+  p.y_out = y_out;
+  p.M = M;
+  p.mpad = round_up(M, 128);
+  p.K = static_cast<int>(K);
+  p.nb = static_cast<int>(K / 32);
+  p.nbp4 = (p.nb + 3) / 4;
+  p.ls = ls;
+  p.eps = eps;
+  p.inv_k = 1.0f / static_cast<float>(K);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool fp8 = fmt == BAT_KV_MXFP8;
+  if (!A) return fp8 ? launch_norm<0, true>(p, sms, s) : launch_norm<0, false>(p, sms, s);
+  if (ls == 3) return fp8 ? launch_norm<1, true>(p, sms, s) : launch_norm<1, false>(p, sms, s);
+  return fp8 ? launch_norm<2, true>(p, sms, s) : launch_norm<2, false>(p, sms, s);
 }
 
 bat_status_t bat_w4a8_gemm(const bat_mxfp8_t* Xq, const bat_mxfp4_t* Wq, void* Y,
