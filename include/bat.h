@@ -367,8 +367,8 @@ typedef struct {
  *              one each.
  * Arithmetic: stored values are used exactly (scales up to 2^39 for KV8, 2^33 for KV4; a larger
  * one, a scale byte 255 or an E4M3 NaN counts as NaN for the rows that see it; products of a
- * weight and a value below 2^-94 may count as 0). q P_q is rounded to bf16 and the softmax weights
- * to bf16 for the products; scores, maxima, sums and outputs are held in fp32 and out is
+ * weight and a value below 2^-94 may count as 0). q P_q is rounded to 11 significant bits and
+ * the softmax weights to bf16 for the products; scores, maxima, sums and outputs are held in fp32 and out is
  * rounded once. Sums run in a fixed order: results do not depend on timing.
  * Errors: BAT_ERR_UNSUPPORTED (a factor split, or K->fmt != V->fmt), BAT_ERR_INVALID_ARG
  * (null pointers, sizes < 1, one factor of a pair only, scale not finite, window or sinks

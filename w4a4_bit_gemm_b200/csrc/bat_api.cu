@@ -14,6 +14,7 @@
 
 #include "../../include/bat.h"
 #include "bat_attn.cuh"
+#include "bat_attn_tile.cuh"
 #include "bat_common.cuh"
 #include "bat_gemm.cuh"
 #include "bat_gemm2.cuh"
@@ -663,8 +664,18 @@ int attn_row_unit(int64_t G, int64_t D) { return G > 8 && D <= 128 ? 16 : 8; }
 size_t attn_part_bytes(int64_t ctas, int64_t rows, int64_t D) {
   const size_t slots = static_cast<size_t>(2 * ctas) * static_cast<size_t>(rows);
   return static_cast<size_t>(round_up(static_cast<int64_t>(slots * D * 4), 256) +
-                             round_up(static_cast<int64_t>(slots * 8), 256));
+                             round_up(static_cast<int64_t>(slots * 8), 256) +
+                             round_up(ctas * static_cast<int64_t>(sizeof(bat::AttnMark)), 256));
 }
+
+// Query rows of a KV head (tokens x heads of the group) from which a chunk goes to the tile
+// kernel.
+constexpr int64_t kAttnTileRows = 64;
+constexpr int kAttnTileCtas = 160;
+bool attn_use_tile(int64_t G, int64_t max_q_len) {
+  return max_q_len > 1 && max_q_len >= (kAttnTileRows + G - 1) / G;
+}
+int64_t attn_tile_rows(int64_t D) { return D <= 128 ? 256 : 128; }
 
 template <class Kernel>
 bat_status_t attn_smem(Kernel k, int dev, int bit, size_t max_bytes) {
@@ -696,7 +707,7 @@ bat_status_t launch_dependent(Kernel k, dim3 grid, dim3 block, size_t smem, cuda
 
 size_t attn_rows_smem(int nb4, int nt, int nb, bool qf, bool of) {
   const size_t r = 8 * nt, dp = 128 * nb4;
-  size_t f = bat::attn::kWarps * r * (dp + 4) + bat::attn::kWarps * r * 2 + r * 2 + r * dp / 2;
+  size_t f = bat::attn::kWarps * r * (dp + 4) + bat::attn::kWarps * r * 2 + r * 2 + r * dp / 2 + r;
   if (qf || of) f += bat::kv::kFacFloats;
   f += static_cast<size_t>(nb) * 1024 * ((qf ? 1 : 0) + (of ? 1 : 0));
   return f * 4;
@@ -717,14 +728,49 @@ bat_status_t launch_attn_rows(bat::AttnParams& p, int dev, int sms, int bit, cud
 }
 
 template <int kTile>
-bat_status_t launch_attn_join(const bat::AttnParams& p, int dev, int bit, int ysplit, cudaStream_t s) {
+bat_status_t launch_attn_join(const bat::AttnParams& p, int dev, int bit, cudaStream_t s) {
   if (p.ctas < 2) return BAT_OK;
   auto k = bat::bat_attn_join_kernel<kTile>;
-  const size_t max_smem = (256 + 4 + bat::kv::kFacFloats + 8 * 1024) * 4;
-  const size_t smem = (p.D + 4 + (p.oa ? bat::kv::kFacFloats + p.nb * 1024 : 0)) * 4;
+  const size_t max_smem = (8 * 260 + bat::kv::kFacFloats + 8 * 1024) * 4;
+  const size_t smem = (8 * 260 + (p.oa ? bat::kv::kFacFloats + p.nb * 1024 : 0)) * 4;
   bat_status_t st = attn_smem(k, dev, bit, max_smem);
   if (st != BAT_OK) return st;
-  return launch_dependent(k, dim3(p.ctas - 1, ysplit), dim3(256), smem, s, p);
+  return launch_dependent(k, dim3(p.ctas - 1, p.unit_rows / 8), dim3(256), smem, s, p);
+}
+
+template <bool kFp8, int kDP>
+bat_status_t launch_attn_tile(bat::AttnParams& p, int dev, int sms, int bit, cudaStream_t s) {
+  using C = bat::attn_tile::Cfg<kDP>;
+  auto k = bat::bat_attn_tile_kernel<kFp8, kDP>;
+  bat_status_t st = attn_smem(k, dev, bit, C::kSmem);
+  if (st != BAT_OK) return st;
+  p.ctas = sms < kAttnTileCtas ? sms : kAttnTileCtas;
+  if (p.qa != nullptr) {
+    bat::AttnQRowsParams q = {};
+    q.q = p.q;
+    q.q_stride = p.q_stride;
+    q.a = p.qa;
+    q.b = p.qb;
+    q.out = const_cast<uint16_t*>(p.qt);
+    q.fac = const_cast<float*>(p.qt_fac);
+    q.rows = p.T * p.Hq;
+    q.Hq = p.Hq;
+    q.D = p.D;
+    q.nb = p.nb;
+    q.ls = p.qls;
+    q.sign = p.q_sign;
+    q.scale_log2 = p.scale_log2;
+    const int64_t want = (q.rows + 7) / 8, cap = static_cast<int64_t>(sms) * 5;
+    bat::bat_attn_q_rows_kernel<<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, s>>>(q);
+    st = cuda_status(cudaGetLastError());
+    if (st != BAT_OK) return st;
+    st = launch_dependent(k, dim3(p.ctas), dim3(bat::attn_tile::kThreads), C::kSmem, s, p);
+  } else {
+    k<<<p.ctas, bat::attn_tile::kThreads, C::kSmem, s>>>(p);
+    st = cuda_status(cudaGetLastError());
+  }
+  if (st != BAT_OK) return st;
+  return launch_attn_join<C::kRows>(p, dev, C::kRows == 256 ? 7 : 8, s);
 }
 
 }  // namespace
@@ -1064,8 +1110,10 @@ bat_status_t bat_kv_dequantize(const void* cache_codes, const void* cache_scales
 size_t bat_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D,
                                         int64_t max_q_len, int has_q_factors) {
   if (T < 1 || Hq < 1 || H < 1 || Hq % H != 0 || D < 32 || D % 32 != 0 || D > 256 || max_q_len < 1) return 0;
-  (void)has_q_factors;
-  return attn_part_bytes(kAttnRowCtas, attn_row_unit(Hq / H, D), D);
+  if (T > kMaxRows / Hq) return 0;
+  if (!attn_use_tile(Hq / H, max_q_len)) return attn_part_bytes(kAttnRowCtas, attn_row_unit(Hq / H, D), D);
+  return attn_part_bytes(kAttnTileCtas, attn_tile_rows(D), D) +
+         (has_q_factors ? static_cast<size_t>(round_up(T * Hq * D * 2, 256) + round_up(T * Hq * 4, 256)) : 0);
 }
 
 bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride,
@@ -1138,14 +1186,32 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   p.ols = ols;
   p.window = static_cast<int>(window < kMaxRows ? window : kMaxRows);
   p.sinks = static_cast<int>(sinks < kMaxRows ? sinks : kMaxRows);
-  p.scale_log2 = scale * 1.4426950408889634f * bat::attn::kUp;
+  p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
+  p.q_sign = scale < 0.0f ? -1.0f : 1.0f;
   const bool fp8 = K->fmt == BAT_KV_MXFP8;
-  const int unit = attn_row_unit(p.G, D);
+  const bool tile = attn_use_tile(p.G, max_q_len);
+  const int unit = tile ? static_cast<int>(attn_tile_rows(D)) : attn_row_unit(p.G, D);
+  const int64_t ctas = tile ? kAttnTileCtas : kAttnRowCtas;
   p.unit_rows = unit;
-  p.head_units = p.Hkv * ((p.G + unit - 1) / unit);
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                       round_up(int64_t{2} * kAttnRowCtas * unit * D * 4, 256));
+  p.head_units = tile ? p.Hkv : p.Hkv * ((p.G + unit - 1) / unit);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.part_o = reinterpret_cast<float*>(ws);
+  ws += round_up(2 * ctas * unit * D * 4, 256);
+  p.part_ml = reinterpret_cast<float*>(ws);
+  ws += round_up(2 * ctas * unit * 8, 256);
+  p.marks = reinterpret_cast<bat::AttnMark*>(ws);
+  ws += round_up(ctas * static_cast<int64_t>(sizeof(bat::AttnMark)), 256);
+  if (tile) {
+    if (Aq) {
+      p.qt = reinterpret_cast<const uint16_t*>(ws);
+      p.qt_fac = reinterpret_cast<const float*>(ws + round_up(T * Hq * D * 2, 256));
+    }
+    if (D > 128)
+      return fp8 ? launch_attn_tile<true, 256>(p, dev, sms, 9, s) : launch_attn_tile<false, 256>(p, dev, sms, 10, s);
+    if (D > 64)
+      return fp8 ? launch_attn_tile<true, 128>(p, dev, sms, 11, s) : launch_attn_tile<false, 128>(p, dev, sms, 12, s);
+    return fp8 ? launch_attn_tile<true, 64>(p, dev, sms, 13, s) : launch_attn_tile<false, 64>(p, dev, sms, 14, s);
+  }
   if (D > 128)
     st = fp8 ? launch_attn_rows<true, 2, 1>(p, dev, sms, 0, s) : launch_attn_rows<false, 2, 1>(p, dev, sms, 1, s);
   else if (unit == 16)
@@ -1153,7 +1219,7 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   else
     st = fp8 ? launch_attn_rows<true, 1, 1>(p, dev, sms, 4, s) : launch_attn_rows<false, 1, 1>(p, dev, sms, 5, s);
   if (st != BAT_OK) return st;
-  return launch_attn_join<0>(p, dev, 6, unit, s);
+  return launch_attn_join<0>(p, dev, 6, s);
 }
 
 bat_status_t bat_rmsnorm_quantize(const void* X, const void* residual, const void* weight, int64_t M,

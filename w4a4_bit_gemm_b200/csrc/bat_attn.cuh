@@ -31,12 +31,23 @@ namespace attn {
 constexpr int kChunk = 128;   // visible tokens a chunk
 constexpr int kWarps = 8;     // row kernel: warps a CTA, 16 tokens of a chunk each
 constexpr int kThreads = 32 * kWarps;
-// The stored elements go to bf16 through their bits, which leaves them 2^120 (E4M3) or 2^126
+// V's stored elements go to bf16 through their bits, which leaves them 2^120 (E4M3) or 2^126
 // (E2M1) too small; the MX scale's multiplication puts that right up to 2^-32, so that
-// scales from 2^-127 to 2^39 (E4M3; 2^33 E2M1) stay within bf16. Scores and outputs are multiplied
-// by 2^32 at the end; a product below 2^-94 may be lost to fp32's smallest number.
+// scales from 2^-127 to 2^39 (E4M3; 2^33 E2M1) stay within bf16. Outputs are multiplied by 2^32
+// at the end; a product below 2^-94 may be lost to fp32's smallest number.
 constexpr float kUp = 0x1p32f;
 }  // namespace attn
+
+// A place in the order of all chunks: sequence, tile, head unit, chunk.
+struct AttnPlace {
+  int b, tile, hu, chunk;
+  int chunks;      // chunks of this unit
+};
+// Where a CTA's run begins, for the joining kernel.
+struct AttnMark {
+  int64_t x, total;  // its first chunk, all chunks
+  AttnPlace place;   // (nothing if x == total)
+};
 
 struct AttnParams {
   const uint16_t* q;       // bf16, token stride q_stride elements, [Hq][D] within a token
@@ -56,6 +67,7 @@ struct AttnParams {
   float* lse;              // fp32 [T][Hq] or null
   float* part_o;           // [2 * ctas][rows][D]
   float* part_ml;          // [2 * ctas][rows][2]
+  AttnMark* marks;         // [ctas]
   int64_t T, num_slots;
   int64_t capacity;        // max_pages * page_size
   int B, max_pages, page_size;
@@ -65,7 +77,10 @@ struct AttnParams {
   int ctas;                // CTAs the chunks are dealt over
   int unit_rows;           // query rows of a unit
   int head_units;          // row kernel: units a token (Hkv * groups of rows); tile kernel: Hkv
-  float scale_log2;        // scale * log2(e) * 2^32
+  float scale_log2;        // |scale| * log2(e)
+  float q_sign;            // sign of the scale, taken into q
+  const uint16_t* qt;      // tile kernel with P_q: f16 rows of q P_q (attn_q_rows), or null
+  const float* qt_fac;     // and their factors, [T][Hq]
 };
 
 // One sequence's facts, from the device arrays, made safe: n >= 0, tokens inside [0, T),
@@ -132,12 +147,6 @@ __device__ __forceinline__ int64_t attn_seq_chunks(const AttnParams& p, const At
   for (int t = 0; t < nt; ++t) c += attn_chunks<kTile>(p, s, t);
   return c * p.head_units;
 }
-
-// A place in the order of all chunks: sequence, tile, head unit, chunk.
-struct AttnPlace {
-  int b, tile, hu, chunk;
-  int chunks;      // chunks of this unit
-};
 
 __device__ __forceinline__ int64_t attn_warp_scan(int64_t v, int lane) {
 #pragma unroll
@@ -239,7 +248,61 @@ __device__ __forceinline__ float attn_exp2(float x) {
   return r;
 }
 
-// ---------------------------------------------------------------- stored elements -> bf16
+// ---------------------------------------------------------------- stored elements -> f16, bf16
+// K's products run in f16: a conversion instruction gives two codes exactly, q (P_q) keeps 11
+// significant bits instead of bf16's 8, and f16's narrow range is no limit since both sides
+// are scaled by powers of two: a row of q by its largest channel, the K values by the largest MX
+// scale of their token (row kernel) or chunk (tile kernel). What falls below f16's range is
+// below 2^-25 of the largest products in the sum it belongs to. V cannot be scaled that way (its
+// channels and tokens are not summed with one maximum), so it goes to bf16, whose range is fp32's.
+__device__ __forceinline__ uint32_t attn_mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The E4M3 pairs (bytes 0, 1) and (bytes 2, 3) of a word as f16 pairs.
+__device__ __forceinline__ void attn_e4m3_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+// The E2M1 pairs of a word's four bytes (low nibble first) as f16 pairs.
+__device__ __forceinline__ void attn_e2m1_f16(uint32_t w, uint32_t (&v)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+      : "r"(w));
+}
+// 2^-d as a pair of f16 (0 below 2^-24).
+__device__ __forceinline__ uint32_t attn_f16_pow2(int d) {
+  const uint32_t h = d <= 14 ? static_cast<uint32_t>(15 - d) << 10 : (d <= 24 ? 1u << (24 - d) : 0u);
+  return h * 0x00010001u;
+}
+// Value of a scale byte.
+__device__ __forceinline__ float attn_scale_value(int byte) {
+  return byte == 255 ? NAN : (byte == 0 ? 0x1p-127f : __uint_as_float(static_cast<uint32_t>(byte) << 23));
+}
+// The power of two that brings a row of largest magnitude m to [2^14, 2^15), and its inverse.
+__device__ __forceinline__ float attn_row_up(float m, float& down) {
+  int e = static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14;  // m < 2^(e + 15)
+  e = e < -100 ? -100 : e;  // (rows below 2^-86 keep fewer bits)
+  down = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+}
+__device__ __forceinline__ uint32_t attn_pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ void attn_mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t attn_mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -254,19 +317,16 @@ __device__ __forceinline__ uint32_t attn_scale_pair(uint32_t byte) {
   return f * 0x00010001u;
 }
 // Bits 15..8 of both halves of x hold E4M3 bytes -> their bits as bf16 (2^120 too small).
-// `nan` collects the largest magnitude: 0x07F0 in a half says that a NaN was among them.
-__device__ __forceinline__ uint32_t attn_e4m3_bits(uint32_t x, uint32_t& nan) {
-  const uint32_t y = (x >> 4) & 0x07F007F0u;
-  nan = __vmaxu2(nan, y);
-  return (x & 0x80008000u) | y;
+// 0x07F0 in a half's magnitude is a NaN.
+__device__ __forceinline__ uint32_t attn_e4m3_bits(uint32_t x) {
+  return (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
 }
 // Bits 15..12 of both halves hold E2M1 codes -> their bits as bf16 (2^126 too small).
 __device__ __forceinline__ uint32_t attn_e2m1_bits(uint32_t x) {
   return (x & 0x80008000u) | ((x >> 6) & 0x01C001C0u);
 }
-__device__ __forceinline__ bool attn_has_nan(uint32_t nan) {
-  return (nan & 0xFFFFu) == 0x07F0u || (nan >> 16) == 0x07F0u;
-}
+// Bit 7 of a byte set where the E4M3 byte of w is a NaN (each magnitude is below 128).
+__device__ __forceinline__ uint32_t attn_e4m3_nan(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
 // The pairs of attn_e4m3_bits with NaN put in for the NaN codes.
 __device__ __forceinline__ uint32_t attn_nan_pair(uint32_t r) {
   if ((r & 0x7FFFu) == 0x07F0u) r |= 0x7FFFu;
@@ -363,8 +423,9 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
   float* so = smem;
   float* sml = so + attn::kWarps * kR * kLdo;
   float* fml = sml + attn::kWarps * kR * 2;  // [kR][2]
-  uint16_t* sq = reinterpret_cast<uint16_t*>(fml + kR * 2);  // [kR][kDP] bf16
-  float* fac = reinterpret_cast<float*>(sq + kR * kDP);      // kFacFloats when factors are given
+  uint16_t* sq = reinterpret_cast<uint16_t*>(fml + kR * 2);  // [kR][kDP] f16
+  float* sqf = reinterpret_cast<float*>(sq + kR * kDP);      // [kR] factors of the q rows
+  float* fac = sqf + kR;                                     // kFacFloats when factors are given
   const bool any_fac = p.qa != nullptr || p.oa != nullptr;
   float* pq = fac + (any_fac ? kv::kFacFloats : 0);
   float* po = pq + (p.qa ? p.nb * 1024 : 0);
@@ -378,11 +439,12 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
     const int64_t total = attn_total<0>(p, lane);
     const int64_t x0 = attn_start(total, blockIdx.x, p.ctas), x1 = attn_start(total, blockIdx.x + 1, p.ctas);
     AttnPlace pl{};
-    if (x0 < x1) pl = attn_locate<0>(p, x0, lane);
+    if (x0 < total) pl = attn_locate<0>(p, x0, lane);
     if (lane == 0) {
       s_place = pl;
       s_run[0] = x0;
       s_run[1] = x1;
+      p.marks[blockIdx.x] = AttnMark{x0, total, pl};
     }
   }
   if (p.qa) kv_build_p(pq, fac, p.qa, p.qb, p.nb, p.qls);
@@ -397,7 +459,6 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
   AttnSeq seq = attn_seq(p, pl.b);
   const int hgs = p.head_units / p.Hkv;  // groups of kR heads of a KV head
   const int row_bytes = kFp8 ? p.D : p.D / 2;
-  const float cs = p.scale_log2;
 
   for (int seg = 0; left > 0; ++seg) {
     const int h = pl.hu / hgs, hg = pl.hu - h * hgs;
@@ -410,18 +471,19 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
     const int last = static_cast<int>(min(static_cast<int64_t>(pl.chunks), first + left));  // chunks [first, last)
     const int32_t* pages = p.table + static_cast<int64_t>(pl.b) * p.max_pages;
 
-    // q rows to shared memory in bf16 (transformed: rounded once more)
+    // q rows (times P_q) in fp32, then in f16 with the row's power of two
     for (int i = threadIdx.x; i < kR * (kDP / 2); i += attn::kThreads) {
       const int n = i / (kDP / 2), d = 2 * (i - n * (kDP / 2));
-      uint32_t w = 0u;
+      float y0 = 0.0f, y1 = 0.0f;
       if (n < nrows && d < p.D) {
         const uint16_t* src = p.q + tok * p.q_stride + static_cast<int64_t>(head0 + n) * p.D;
         if (p.qa == nullptr) {
-          w = *reinterpret_cast<const uint32_t*>(src + d);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(src + d);
+          y0 = bf16lo(w);
+          y1 = bf16hi(w);
         } else {
           const uint32_t* s2 = reinterpret_cast<const uint32_t*>(src + (d & ~31));
           const float* pb = pq + (d >> 5) * 1024 + (d & 31);
-          float y0 = 0.0f, y1 = 0.0f;
 #pragma unroll 4
           for (int k = 0; k < 16; ++k) {
             const uint32_t x = s2[k];
@@ -432,28 +494,51 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
             y0 = __fmaf_rn(bf16hi(x), c1.x, y0);
             y1 = __fmaf_rn(bf16hi(x), c1.y, y1);
           }
-          w = attn_pack(y0, y1);
         }
       }
-      *reinterpret_cast<uint32_t*>(sq + n * kDP + d) = w;
+      *reinterpret_cast<float2*>(so + n * kLdo + d) = make_float2(y0, y1);
     }
     __syncthreads();
-    // this lane's q operands: heads r (and r + 8), the channels of its K words
-    uint32_t qf[kNT][kNB4][16];
+    for (int n = warp; n < kR; n += attn::kWarps) {
+      float y[kDP / 32], mx = 0.0f;
 #pragma unroll
-    for (int t = 0; t < kNT; ++t)
+      for (int k = 0; k < kDP / 64; ++k) {
+        const float2 v = *reinterpret_cast<const float2*>(so + n * kLdo + 64 * k + 2 * lane);
+        y[2 * k] = v.x;
+        y[2 * k + 1] = v.y;
+        mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
+      }
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      float down;
+      const float up = attn_row_up(mx, down) * p.q_sign;
+#pragma unroll
+      for (int k = 0; k < kDP / 64; ++k)
+        *reinterpret_cast<uint32_t*>(sq + n * kDP + 64 * k + 2 * lane) = attn_pack_f16(y[2 * k] * up, y[2 * k + 1] * up);
+      if (lane == 0) sqf[n] = down * p.scale_log2;
+    }
+    __syncthreads();
+    // this lane's q operands: heads r (and r + 8), the channels of its K words; the factors
+    // of its score columns
+    uint32_t qf[kNT][kNB4][16];
+    float cs[kNT][2];
+#pragma unroll
+    for (int t = 0; t < kNT; ++t) {
+      cs[t][0] = sqf[8 * t + 2 * c];
+      cs[t][1] = sqf[8 * t + 2 * c + 1];
 #pragma unroll
       for (int b4 = 0; b4 < kNB4; ++b4) {
-        const uint16_t* src = sq + (8 * t + r) * kDP + 32 * (c + 4 * b4);
+        const uint4* src = reinterpret_cast<const uint4*>(sq + (8 * t + r) * kDP + 32 * (c + 4 * b4));
 #pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          // channels (x0, x1) and (x2, x3) of k-step s: the halves attn_*_bits leave in a pair
-          const int w0 = kFp8 ? 4 * s : 8 * (s >> 1) + 2 * (s & 1);
-          const int x0 = w0, x1 = kFp8 ? w0 + 2 : w0 + 4, x2 = w0 + 1, x3 = kFp8 ? w0 + 3 : w0 + 5;
-          qf[t][b4][2 * s] = src[x0] | static_cast<uint32_t>(src[x1]) << 16;
-          qf[t][b4][2 * s + 1] = src[x2] | static_cast<uint32_t>(src[x3]) << 16;
+        for (int s = 0; s < 4; ++s) {
+          const uint4 w = src[s];
+          qf[t][b4][4 * s] = w.x;
+          qf[t][b4][4 * s + 1] = w.y;
+          qf[t][b4][4 * s + 2] = w.z;
+          qf[t][b4][4 * s + 3] = w.w;
         }
       }
+    }
 
     float m[kNT][2], l[kNT][2], o[kNT][kMT][4];
 #pragma unroll
@@ -527,44 +612,41 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
       float s[kNT][4];
 #pragma unroll
       for (int t = 0; t < kNT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
-      uint32_t nan[2] = {0u, 0u};
+      int top[2];  // the tokens' largest scale bytes (the quad holds a token's blocks)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        top[x] = static_cast<int>(g.ks[x][0]);
+        if (kNB4 == 2) top[x] = max(top[x], static_cast<int>(g.ks[x][kNB4 - 1]));
+        top[x] = max(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+        top[x] = max(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
+      }
 #pragma unroll
       for (int b4 = 0; b4 < kNB4; ++b4) {
-        const uint32_t f0 = attn_scale_pair<kFp8>(g.ks[0][b4]), f1 = attn_scale_pair<kFp8>(g.ks[1][b4]);
+        const uint32_t f0 = attn_f16_pow2(top[0] - static_cast<int>(g.ks[0][b4]));
+        const uint32_t f1 = attn_f16_pow2(top[1] - static_cast<int>(g.ks[1][b4]));
 #pragma unroll
-        for (int st = 0; st < 8; ++st) {
-          uint32_t a[2][2];
+        for (int w = 0; w < kKw; ++w) {
+          // a word holds one k-step's (E4M3) or two k-steps' (E2M1) operands of this lane
+          uint32_t a[2][4];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const uint32_t f = x ? f1 : f0;
-            if (kFp8) {
-              const uint32_t w = g.k[x][b4][st];
-              a[x][0] = attn_mul_bf16x2(attn_e4m3_bits(w << 8, nan[x]), f);
-              a[x][1] = attn_mul_bf16x2(attn_e4m3_bits(w, nan[x]), f);
-            } else {
-              const uint32_t w = g.k[x][b4][st >> 1] << (st & 1 ? 4 : 12);
-              a[x][0] = attn_mul_bf16x2(attn_e2m1_bits(w), f);
-              const uint32_t w2 = st & 1 ? g.k[x][b4][st >> 1] : g.k[x][b4][st >> 1] << 8;
-              a[x][1] = attn_mul_bf16x2(attn_e2m1_bits(w2), f);
-            }
+            if (kFp8)
+              attn_e4m3_f16(g.k[x][b4][w], a[x][0], a[x][1]);
+            else
+              attn_e2m1_f16(g.k[x][b4][w], a[x]);
+#pragma unroll
+            for (int e = 0; e < (kFp8 ? 2 : 4); ++e) a[x][e] = attn_mul_f16x2(a[x][e], x ? f1 : f0);
           }
 #pragma unroll
-          for (int t = 0; t < kNT; ++t)
-            attn_mma(s[t], a[0][0], a[1][0], a[0][1], a[1][1], qf[t][b4][2 * st], qf[t][b4][2 * st + 1]);
-        }
-      }
-      if (kFp8) {
-        // a stored NaN makes its token's scores NaN
-        const unsigned b0 = __ballot_sync(0xffffffffu, attn_has_nan(nan[0]));
-        const unsigned b1 = __ballot_sync(0xffffffffu, attn_has_nan(nan[1]));
-        if (b0 | b1) {
+          for (int e = 0; e < (kFp8 ? 2 : 4); e += 2) {
+            const int st = kFp8 ? w : 2 * w + e / 2;
 #pragma unroll
-          for (int t = 0; t < kNT; ++t) {
-            if (b0 >> (4 * r) & 15u) s[t][0] = s[t][1] = NAN;
-            if (b1 >> (4 * r) & 15u) s[t][2] = s[t][3] = NAN;
+            for (int t = 0; t < kNT; ++t)
+              attn_mma_f16(s[t], a[0][e], a[1][e], a[0][e + 1], a[1][e + 1], qf[t][b4][2 * st], qf[t][b4][2 * st + 1]);
           }
         }
       }
+      const float kv0 = attn_scale_value(top[0]), kv1 = attn_scale_value(top[1]);
       const bool see0 = __shfl_sync(0xffffffffu, rows_now, r) >= 0;
       const bool see1 = __shfl_sync(0xffffffffu, rows_now, r + 8) >= 0;
       load_k(rows_next);
@@ -574,10 +656,10 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
         float x[4], mx[2];
-        x[0] = see0 ? s[t][0] * cs : -INFINITY;
-        x[1] = see0 ? s[t][1] * cs : -INFINITY;
-        x[2] = see1 ? s[t][2] * cs : -INFINITY;
-        x[3] = see1 ? s[t][3] * cs : -INFINITY;
+        x[0] = see0 ? s[t][0] * kv0 * cs[t][0] : -INFINITY;
+        x[1] = see0 ? s[t][1] * kv0 * cs[t][1] : -INFINITY;
+        x[2] = see1 ? s[t][2] * kv1 * cs[t][0] : -INFINITY;
+        x[3] = see1 ? s[t][3] * kv1 * cs[t][1] : -INFINITY;
         mx[0] = fmaxf(x[0], x[2]);
         mx[1] = fmaxf(x[1], x[3]);
 #pragma unroll
@@ -624,7 +706,7 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-          for (int k = 0; k < kVw; ++k) nv4 |= (g.v[x][k] & 0x7F7F7F7Fu) + 0x01010101u;
+          for (int k = 0; k < kVw; ++k) nv4 |= attn_e4m3_nan(g.v[x][k]);
         slow = __any_sync(0xffffffffu, (nv4 & 0x80808080u) != 0u);
       }
 #pragma unroll
@@ -637,9 +719,8 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
           if (kFp8) {
             const int by = d & 3;
             const uint32_t sel = static_cast<uint32_t>(by) << 4 | static_cast<uint32_t>(4 + by) << 12;
-            uint32_t dummy = 0u;
-            lo = attn_e4m3_bits(__byte_perm(g.v[0][d >> 2], g.v[1][d >> 2], sel), dummy);
-            hi = attn_e4m3_bits(__byte_perm(g.v[2][d >> 2], g.v[3][d >> 2], sel), dummy);
+            lo = attn_e4m3_bits(__byte_perm(g.v[0][d >> 2], g.v[1][d >> 2], sel));
+            hi = attn_e4m3_bits(__byte_perm(g.v[2][d >> 2], g.v[3][d >> 2], sel));
             if (slow) {
               lo = attn_nan_pair(lo);
               hi = attn_nan_pair(hi);
@@ -739,49 +820,33 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
 
 // ---------------------------------------------------------------- joining partial results
 // CTA (x, y): if CTA x + 1's run begins inside a unit, and no earlier run does, the parts
-// of that unit (the last of CTA x, then the first of x + 1, x + 2, ...) are joined here, rows
-// y, y + gridDim.y, ...  kTile as in the kernel that wrote them.
+// of that unit (the last of CTA x, then the first of x + 1, x + 2, ...) are joined here, a warp a
+// row. kTile as in the kernel that wrote them. Bound: the parts' bytes, or launch latency.
 template <int kTile>
 __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) {
   extern __shared__ __align__(16) float smem[];
-  __shared__ AttnPlace s_place;
-  __shared__ int64_t s_total, s_start;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i1 = blockIdx.x + 1;
-  if (threadIdx.x < 32) {
-    const int64_t total = attn_total<kTile>(p, lane);
-    const int64_t x = attn_start(total, i1, p.ctas);
-    AttnPlace pl{};
-    if (x < total) pl = attn_locate<kTile>(p, x, lane);
-    if (lane == 0) {
-      s_place = pl;
-      s_total = total;
-      s_start = x;
-    }
-  }
-  __syncthreads();
-  const int64_t total = s_total, x = s_start;
+  float* so = smem + warp * 260;  // [D] of this warp's row, its maximum and sum
+  float* po = nullptr;
+  grid_dependency_wait();
+  const AttnMark mk = p.marks[i1];
+  const int64_t total = mk.total, x = mk.x;
   if (x >= total) return;
-  const AttnPlace pl = s_place;
+  const AttnPlace pl = mk.place;
   const int64_t u0 = x - pl.chunk, u1 = u0 + pl.chunks;
   if (pl.chunk == 0 || attn_start(total, i1 - 1, p.ctas) > u0) return;  // no split here, or an earlier CTA's
   int end = i1 + 1;  // parts of CTAs [i1 - 1, end)
   while (end < p.ctas && attn_start(total, end, p.ctas) < u1) ++end;
-  // CTA i1 - 1 may hold nothing of the unit when its run is empty
-  const int rows = p.unit_rows;
-  float* so = smem;              // [1][D]
-  float* sml = so + p.D;         // [2]
-  float* fac = sml + 4;
-  float* po = nullptr;
   if (p.oa) {
-    po = fac + kv::kFacFloats;
-    kv_build_p(po, fac, p.oa, p.ob, p.nb, p.ols);
+    po = smem + 8 * 260 + kv::kFacFloats;
+    kv_build_p(po, smem + 8 * 260, p.oa, p.ob, p.nb, p.ols);
   }
+  const int rows = p.unit_rows;
   const AttnSeq seq = attn_seq(p, pl.b);
-  grid_dependency_wait();
   const int hgs = p.head_units / p.Hkv;
   const int h = pl.hu / hgs, hg = pl.hu - h * hgs;
-  for (int rr = blockIdx.y; rr < rows; rr += gridDim.y) {
+  for (int rr = blockIdx.y * 8 + warp; rr < rows; rr += gridDim.y * 8) {
     int64_t tok;
     int head;
     if (kTile) {
@@ -795,42 +860,65 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
       tok = seq.t0 + pl.tile;
       head = h * p.G + hg * rows + rr;
     }
-    auto slot_of = [&](int i) -> int64_t {
-      // the unit is the first of CTA i's run if the run begins inside the unit (or at it)
-      return 2 * static_cast<int64_t>(i) + (attn_start(total, i, p.ctas) >= u0 ? 0 : 1);
-    };
-    float mm = -INFINITY;
+    // running over the parts in order: maximum, sum and o, as in the kernels
+    float mm = -INFINITY, sum = 0.0f;
+    float2 acc[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.0f, 0.0f);
     bool bad = false;
     for (int i = i1 - 1; i < end; ++i) {
-      if (attn_start(total, i, p.ctas) >= attn_start(total, i + 1, p.ctas)) continue;
-      const float* ml = p.part_ml + (slot_of(i) * rows + rr) * 2;
-      mm = fmaxf(mm, ml[0]);
-      bad |= ml[1] != ml[1];
+      const int64_t xi = attn_start(total, i, p.ctas);
+      if (xi >= attn_start(total, i + 1, p.ctas)) continue;  // an empty run
+      // the unit is the first of CTA i's run if the run begins inside the unit (or at it)
+      const int64_t at = (2 * static_cast<int64_t>(i) + (xi >= u0 ? 0 : 1)) * rows + rr;
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+      float2 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (64 * k + 2 * lane < p.D) v[k] = *reinterpret_cast<const float2*>(p.part_o + at * p.D + 64 * k + 2 * lane);
+      bad |= ml.y != ml.y;
+      if (ml.x == -INFINITY) continue;  // saw nothing
+      const float mn = fmaxf(mm, ml.x);
+      const float fo = attn_exp2(mm - mn), fi = attn_exp2(ml.x - mn);
+      mm = mn;
+      sum = sum * fo + ml.y * fi;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (64 * k + 2 * lane < p.D) {
+          acc[k].x = acc[k].x * fo + v[k].x * fi;
+          acc[k].y = acc[k].y * fo + v[k].y * fi;
+        }
     }
-    for (int d = threadIdx.x; d < p.D; d += blockDim.x) {
-      float acc = 0.0f, sum = 0.0f;
-      for (int i = i1 - 1; i < end; ++i) {
-        if (attn_start(total, i, p.ctas) >= attn_start(total, i + 1, p.ctas)) continue;
-        const int64_t s = slot_of(i) * rows + rr;
-        const float mi = p.part_ml[s * 2];
-        const float f = mi == -INFINITY ? 0.0f : attn_exp2(mi - mm);
-        if (f != 0.0f || mi != mi) acc = __fmaf_rn(p.part_o[s * p.D + d], f, acc);
-        sum = __fmaf_rn(p.part_ml[s * 2 + 1], f, sum);
-      }
-      if (bad) acc = sum = NAN;
-      so[d] = acc;
-      if (d == 0) {
-        sml[0] = mm;
-        sml[1] = sum;
-      }
+    if (bad) sum = NAN;
+    const float inv = sum > 0.0f ? attn::kUp / sum : (sum == 0.0f ? 0.0f : sum);
+    uint16_t* dst = p.out + (tok * p.Hq + head) * p.D;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      acc[k].x *= inv;
+      acc[k].y *= inv;
+      if (po != nullptr && 64 * k + 2 * lane < p.D) *reinterpret_cast<float2*>(so + 64 * k + 2 * lane) = acc[k];
     }
-    __syncthreads();
-    attn_finish(p, so, p.D, sml, 1, po, [&](int, int64_t& t, int& hd) {
-      t = tok;
-      hd = head;
-      return true;
-    });
-    __syncthreads();
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int d = 64 * k + 2 * lane;
+      if (d >= p.D) break;
+      if (po != nullptr) {
+        const float* src = so + (d & ~31);
+        const float* pb = po + (d >> 5) * 1024 + (d & 31);
+        acc[k] = make_float2(0.0f, 0.0f);
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j) {
+          const float2 cf = *reinterpret_cast<const float2*>(pb + 32 * j);
+          acc[k].x = __fmaf_rn(src[j], cf.x, acc[k].x);
+          acc[k].y = __fmaf_rn(src[j], cf.y, acc[k].y);
+        }
+      }
+      *reinterpret_cast<uint32_t*>(dst + d) = attn_pack(acc[k].x, acc[k].y);
+    }
+    __syncwarp();
+    if (p.lse && lane == 0)
+      p.lse[tok * p.Hq + head] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * 0.69314718055994531f;
   }
 }
 
