@@ -1177,6 +1177,11 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   p.B = static_cast<int>(B);
   p.max_pages = static_cast<int>(max_pages);
   p.page_size = static_cast<int>(page_size);
+  // division by a constant for 31-bit numerators: l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1
+  int pl = 0;
+  while ((int64_t{1} << pl) < page_size) ++pl;
+  p.page_shift = 31 + pl;
+  p.page_mul = static_cast<uint32_t>((uint64_t{1} << (31 + pl)) / static_cast<uint64_t>(page_size) + 1);
   p.Hq = static_cast<int>(Hq);
   p.Hkv = static_cast<int>(H);
   p.G = static_cast<int>(Hq / H);

@@ -71,6 +71,8 @@ struct AttnParams {
   int64_t T, num_slots;
   int64_t capacity;        // max_pages * page_size
   int B, max_pages, page_size;
+  uint32_t page_mul;       // j / page_size = (j * page_mul) >> page_shift for 0 <= j < 2^31
+  int page_shift;
   int Hq, Hkv, G, D, nb;
   int qls, ols;
   int window, sinks;       // window 0: none
@@ -231,15 +233,21 @@ __device__ __forceinline__ void attn_next_unit(const AttnParams& p, AttnPlace& p
   pl.chunks = attn_chunks<kTile>(p, s, pl.tile);
 }
 
-// Cache row (slot * Hkv + head) of token j of a sequence, or -1 for a page outside the cache.
-__device__ __forceinline__ int attn_cache_row(const AttnParams& p, const int32_t* pages, int j, int h) {
-  const int pg = j / p.page_size;
-  const int64_t slot = static_cast<int64_t>(__ldg(pages + pg)) * p.page_size + (j - pg * p.page_size);
+// Cache row (slot * Hkv + head) of token j of a sequence, or -1 for a page outside the cache, in
+// two steps, so that the table's entry can be on its way while other work is done.
+__device__ __forceinline__ int attn_page_of(const AttnParams& p, int j) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(j)) * p.page_mul) >> p.page_shift);
+}
+__device__ __forceinline__ int attn_row_at(const AttnParams& p, int page, int j, int h) {
+  const int64_t slot = static_cast<int64_t>(page) * p.page_size + (j - attn_page_of(p, j) * p.page_size);
   if (slot < 0 || slot >= p.num_slots) {
     atomicOr(&g_dev_error, kErrBadIndex);
     return -1;
   }
   return static_cast<int>(slot * p.Hkv + h);
+}
+__device__ __forceinline__ int attn_cache_row(const AttnParams& p, const int32_t* pages, int j, int h) {
+  return attn_row_at(p, __ldg(pages + attn_page_of(p, j)), j, h);
 }
 
 __device__ __forceinline__ float attn_exp2(float x) {

@@ -6,9 +6,9 @@
 // tile. Its visible tokens come in chunks of 128. Warp roles:
 //   warps 0-3, 4-7  softmax of tile 0 / 1, one row a thread: S from TMEM, weights back into
 //                   S's columns as the A operand of the second product; q staging and the output
-//   warps 8-11      K and V: page lookup, loads of codes and scales two steps ahead, expansion
+//   warps 8-15      K and V: page lookup, loads of codes and scales a chunk ahead, expansion
 //                   to f16 (K) and bf16 (V) in swizzled shared memory
-//   warp 12         issues the MMAs and owns TMEM
+//   warp 16         issues the MMAs and owns TMEM
 // Per chunk and tile: S = q K^T (M 128, N 128, K = D, kind::f16 on f16) and
 // o += P V (N = D, K = 128, kind::f16 on bf16, P from TMEM). The MMAs of one tile run while the
 // other tile's warps are in their softmax. The maximum is lazy: o is rescaled only when the
@@ -27,10 +27,11 @@ namespace bat {
 
 namespace attn_tile {
 constexpr int kPanelBytes = 128 * 128;  // 128 rows of 64 16-bit channels, 128-byte swizzle
-constexpr int kThreads = 512;           // 13 warps work; the register split goes by four warps
+constexpr int kLoadWarps = 8;
+constexpr int kThreads = 640;  // 17 warps work; the register split goes by four warps
+constexpr int kRegsSoftmax = 120, kRegsLoad = 104, kRegsMma = 32;
+static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsMma <= 5 * 96, "the split stays within the launch's registers");
 constexpr int kInfo = 8;                // chunks whose notes are kept (see the ring's order)
-constexpr int kRegsSoftmax = 184, kRegsLoad = 104, kRegsMma = 40;
-static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsMma <= 4 * 128, "the split stays within the launch's registers");
 
 template <int kDP>
 struct Cfg {
@@ -70,12 +71,19 @@ __device__ __forceinline__ void attn_mma_ts(uint32_t d, uint32_t a, uint64_t b, 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// Loader warps only: a barrier of its 128 threads that also agrees on `ok`, so that all of them
+// One lane of a converged warp. (An MMA issued under a plain lane test takes about 400 cycles of
+// its thread; the compiler has to assume that several lanes get there.)
+__device__ __forceinline__ bool attn_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Loader warps only: a barrier of their 256 threads that also agrees on `ok`, so that all of them
 // leave together after a wait that ran out.
 __device__ __forceinline__ bool attn_load_sync(bool ok) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 128, p;\n\t"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 256, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"(static_cast<uint32_t>(ok))
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
   allow_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 4);
+      mbar_init(full(s), attn_tile::kLoadWarps);
       mbar_init(empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -230,11 +238,11 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(smem_u32(&s_tmem), 512);
     tmem_relinquish();
   }
-  if (warp == 13) {
+  if (warp == 15) {
     const int64_t total = attn_total<kTile>(p, lane);
     const int64_t x0 = attn_start(total, blockIdx.x, p.ctas), x1 = attn_start(total, blockIdx.x + 1, p.ctas);
     AttnPlace pl{};
@@ -284,43 +292,40 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
       const int head = run.pl.hu * p.G + static_cast<int>(row - rt * p.G);
       const int base = run.seq.len - run.seq.n;
       const int pos = valid ? base + static_cast<int>(rt) : -1;
-      // ---- q row to shared memory
+      // ---- q row to shared memory (read twice: for its largest channel, and converted)
       float cs = 0.0f;
       {
         const uint32_t qrow = q_base + (t * C::kPanels) * attn_tile::kPanelBytes + rr * 128;
-        uint4 w[kDP / 8];
-        if (p.qt != nullptr) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.qt + (tok * p.Hq + head) * p.D);
-#pragma unroll
-          for (int v = 0; v < kDP / 8; ++v)
-            w[v] = valid && 8 * v < p.D ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
-          cs = valid ? __ldg(p.qt_fac + tok * p.Hq + head) : 0.0f;
-        } else {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + tok * p.q_stride + static_cast<int64_t>(head) * p.D);
+        const bool ready = p.qt != nullptr;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            ready ? p.qt + (tok * p.Hq + head) * p.D : p.q + tok * p.q_stride + static_cast<int64_t>(head) * p.D);
+        float up = 1.0f;
+        if (!ready) {
           float mx = 0.0f;
-#pragma unroll
+#pragma unroll 8
           for (int v = 0; v < kDP / 8; ++v) {
-            w[v] = valid && 8 * v < p.D ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t e[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+            const uint4 w = valid && 8 * v < p.D ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(e[k])), fabsf(bf16hi(e[k]))));
           }
           float down;
-          const float up = attn_row_up(mx, down) * p.q_sign;
+          up = attn_row_up(mx, down) * p.q_sign;
           cs = down * p.scale_log2;
-#pragma unroll
-          for (int v = 0; v < kDP / 8; ++v) {
-            w[v].x = attn_pack_f16(bf16lo(w[v].x) * up, bf16hi(w[v].x) * up);
-            w[v].y = attn_pack_f16(bf16lo(w[v].y) * up, bf16hi(w[v].y) * up);
-            w[v].z = attn_pack_f16(bf16lo(w[v].z) * up, bf16hi(w[v].z) * up);
-            w[v].w = attn_pack_f16(bf16lo(w[v].w) * up, bf16hi(w[v].w) * up);
-          }
+        } else if (valid) {
+          cs = __ldg(p.qt_fac + tok * p.Hq + head);
         }
-#pragma unroll
+#pragma unroll 8
         for (int v = 0; v < kDP / 8; ++v) {
+          uint4 w = valid && 8 * v < p.D ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
+          if (!ready) {
+            w.x = attn_pack_f16(bf16lo(w.x) * up, bf16hi(w.x) * up);
+            w.y = attn_pack_f16(bf16lo(w.y) * up, bf16hi(w.y) * up);
+            w.z = attn_pack_f16(bf16lo(w.z) * up, bf16hi(w.z) * up);
+            w.w = attn_pack_f16(bf16lo(w.w) * up, bf16hi(w.w) * up);
+          }
           const uint32_t a = qrow + (v >> 3) * attn_tile::kPanelBytes + (((v & 7) ^ (rr & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[v].x), "r"(w[v].y), "r"(w[v].z),
-                       "r"(w[v].w)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
                        : "memory");
         }
       }
@@ -383,41 +388,44 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
         tc_fence_after();
         // V of the chunk before is complete: its notes
         if (i > 0 && *reinterpret_cast<volatile int*>(&notes[(n_c - 1) % attn_tile::kInfo].any)) see_nan(n_c - 1, chunk - 1);
-        uint32_t s[4][32];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(s_col(t) + lane_base + 32 * k, s[k]);
-        tmem_wait_ld();
         const AttnNote& note = notes[n_c % attn_tile::kInfo];
         const float cc = fmaxf(cs * note.kfac, 1e-37f);
         const int i0 = chunk * 128;
+        // masked columns go to TMEM as -inf, so that the two passes below need no test (S is read
+        // twice, 32 columns at a time, instead of being held: 120 registers a thread do)
         const bool whole = (i0 >= all_lo || i0 + 128 <= sp.ns) && i0 + 128 <= all_hi;
-        if (!whole) {
+        const bool hidden = *reinterpret_cast<const volatile int*>(&note.any) != 0;
+        if (!whole || hidden) {
           const int c_hi = v_hi - i0, c_lo = v_lo - i0, c_sink = v_sink - i0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
+#pragma unroll 1
+          for (int k = 0; k < 128; k += 32) {
+            uint32_t s[32];
+            tmem_ld_32x32b_x32(s_col(t) + lane_base + k, s);
+            tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const int c = 32 * k + j;
-              if (!(c < c_hi && (c >= c_lo || c < c_sink))) s[k][j] = 0xFF800000u;
+              const int c = k + j;
+              if (!(c < c_hi && (c >= c_lo || c < c_sink))) s[j] = 0xFF800000u;
+              if (hidden && (note.tok[c] >> 31)) s[j] = 0xFF800000u;
             }
+            tmem_st_32x32b_x16(s_col(t) + lane_base + k, reinterpret_cast<const uint32_t(&)[16]>(s[0]));
+            tmem_st_32x32b_x16(s_col(t) + lane_base + k + 16, reinterpret_cast<const uint32_t(&)[16]>(s[16]));
+          }
+          tmem_wait_st();
         }
-        if (*reinterpret_cast<const volatile int*>(&note.any)) {
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 128; k += 32) {
+          uint32_t s[32];
+          tmem_ld_32x32b_x32(s_col(t) + lane_base + k, s);
+          tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (note.tok[32 * k + j] >> 31) s[k][j] = 0xFF800000u;
+          for (int j = 0; j < 32; j += 4) {
+            asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[0]) : "f"(__uint_as_float(s[j])), "f"(__uint_as_float(s[j + 1])));
+            asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[1]) : "f"(__uint_as_float(s[j + 2])), "f"(__uint_as_float(s[j + 3])));
+          }
         }
-        float mx[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          mx[k] = __uint_as_float(s[k][0]);
-#pragma unroll
-          for (int j = 1; j < 31; j += 2)
-            asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[k]) : "f"(__uint_as_float(s[k][j])), "f"(__uint_as_float(s[k][j + 1])));
-          mx[k] = fmaxf(mx[k], __uint_as_float(s[k][31]));
-        }
-        const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * cc;
+        const float mn = fmaxf(mx[0], mx[1]) * cc;
         if (i == 0) {
           m = mn;
         } else {
@@ -445,17 +453,20 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
         const float ms = m == -INFINITY ? 0.0f : m;
         const uint64_t c2 = pack2(cc, cc), m2 = pack2(-ms, -ms);
         uint64_t sum2 = pack2(l0, l1);
+        // weights over the columns already read: S's columns 32 k .. give way to 16 k ..
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t w[16];
+          uint32_t s[32], w[16];
+          tmem_ld_32x32b_x32(s_col(t) + lane_base + 32 * k, s);
+          tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float a, b;
-            unpack2(ffma2(pack2(__uint_as_float(s[k][2 * j]), __uint_as_float(s[k][2 * j + 1])), c2, m2), a, b);
+            unpack2(ffma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, m2), a, b);
             a = attn_exp2(a);
             b = attn_exp2(b);
             sum2 = fadd2(sum2, pack2(a, b));
-            w[j] = attn_pack(a, b);  // bf16: off by half a step 2^-9 of each weight, unbiased
+            w[j] = attn_pack(a, b);  // bf16: off by half a step 2^-8 of each weight, unbiased
           }
           tmem_st_32x32b_x16(s_col(t) + lane_base + 16 * k, w);
         }
@@ -567,15 +578,17 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
       __syncwarp();
       run.next_unit(p, n);
     }
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // ================================================================ K and V
-    setmaxnreg_dec<attn_tile::kRegsLoad>();
+    setmaxnreg_inc<attn_tile::kRegsLoad>();
     constexpr int kLpt = kFp8 ? kDP / 16 : kDP / 32;     // lanes a token: 16 bytes of codes each
     constexpr int kTpi = 32 / kLpt;                      // tokens a load instruction
-    constexpr int kTasks = kLpt;                         // 16-byte pieces a thread (a warp has 32 tokens)
-    constexpr int kBatch = kTasks < 8 ? kTasks : 8;
+    constexpr int kTasks = 16 / kTpi;                    // 16-byte pieces a thread (a warp has 16 tokens)
+    static_assert(kTasks >= 1 && 16 % kTpi == 0, "a warp's tokens are whole load instructions");
+    constexpr int kBatch = kTasks < 4 ? kTasks : 4;
     constexpr int kNB = kTasks / kBatch;                 // batches a tile: 1 or 2
-    const int lw = warp - 8, tid = threadIdx.x - 256;    // token of this thread in the lookups
+    const int lw = warp - 8, tid = threadIdx.x - 256;
+    const int my_tok = tid & 127, my_kv = tid >> 7;      // token and side (K or V) of this thread's lookups
     const int row_bytes = kFp8 ? p.D : p.D / 2;
     // the lanes of a quarter-warp take the pieces of one panel of neighbouring tokens, so that
     // their 16-byte stores fall on different banks of the swizzled rows
@@ -584,66 +597,78 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     const int sub = (lane >> 3) / C::kPanels * (8 / kPp) + lane % 8 / kPp;
     const bool has = piece * 16 < row_bytes;
     const int pblk = kFp8 ? piece >> 1 : piece;          // its 32-channel block
+    const uint8_t* my_scales = my_kv ? p.v_scales : p.k_scales;
     bool ok = true;
     uint4 buf[2][kBatch];
 
-    auto lookup = [&](bool& bad) -> int {
-      bad = false;
-      if (run.left <= 0) return -1;
-      const int idx = run.pl.chunk * 128 + tid;
-      if (idx >= run.nv) return -1;
-      const int r = attn_cache_row(p, p.table + static_cast<int64_t>(run.pl.b) * p.max_pages, run.span.token(idx),
-                                   run.pl.hu);
-      bad = r < 0;
+    // this thread's token of the chunk the run stands at: its place (-1: none), the table's entry
+    int j_ahead = -1, h_ahead = 0, page_ahead = 0;
+    auto look = [&]() {
+      j_ahead = -1;
+      if (run.left <= 0) return;
+      const int idx = run.pl.chunk * 128 + my_tok;
+      if (idx >= run.nv) return;
+      j_ahead = run.span.token(idx);
+      h_ahead = run.pl.hu;
+      page_ahead = __ldg(p.table + static_cast<int64_t>(run.pl.b) * p.max_pages + attn_page_of(p, j_ahead));
+    };
+    auto found = [&](bool& bad) -> int {
+      const int r = j_ahead >= 0 ? attn_row_at(p, page_ahead, j_ahead, h_ahead) : -1;
+      bad = j_ahead >= 0 && r < 0;
       return r;
     };
-    uint32_t ks[kDP / 32], vs[kDP / 32];
+    uint32_t sc[kDP / 32];
     auto load_scales = [&](int row) {
 #pragma unroll
-      for (int b = 0; b < kDP / 32; ++b) {
-        const bool h = row >= 0 && b < p.nb;
-        ks[b] = h ? __ldg(p.k_scales + static_cast<int64_t>(row) * p.nb + b) : 0u;
-        vs[b] = h ? __ldg(p.v_scales + static_cast<int64_t>(row) * p.nb + b) : 0u;
-      }
+      for (int b = 0; b < kDP / 32; ++b)
+        sc[b] = row >= 0 && b < p.nb ? __ldg(my_scales + static_cast<int64_t>(row) * p.nb + b) : 0u;
     };
     // scales, the largest of K's, and the notes of chunk c (parity c & 1), before a barrier
     auto publish = [&](uint32_t c, bool bad) {
       int top = 0;
 #pragma unroll
       for (int b = 0; b < kDP / 32; ++b) {
-        s_scale[c & 1][0][tid][b] = static_cast<uint8_t>(ks[b]);
-        s_scale[c & 1][1][tid][b] = static_cast<uint8_t>(vs[b]);
+        s_scale[c & 1][my_kv][my_tok][b] = static_cast<uint8_t>(sc[b]);
         // NaN scales stand for themselves and do not set the common scale
-        if (ks[b] != 255u) top = max(top, static_cast<int>(ks[b]));
+        if (sc[b] != 255u) top = max(top, static_cast<int>(sc[b]));
       }
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) s_top[c & 1][lw] = top;
-      AttnNote& nt = notes[c % attn_tile::kInfo];
-      nt.tok[tid] = bad ? 0x80000000u : 0u;
-      if (tid == 0) nt.any = 0;
+      if (my_kv == 0) {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) s_top[c & 1][lw] = top;
+        AttnNote& nt = notes[c % attn_tile::kInfo];
+        nt.tok[my_tok] = bad ? 0x80000000u : 0u;
+        if (tid == 0) nt.any = 0;
+      }
     };
     auto load_batch = [&](int par, const uint8_t* codes, int b, uint4 (&dst)[kBatch]) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int row = s_rows[par][32 * lw + (b * kBatch + k) * kTpi + sub];
+        const int row = s_rows[par][16 * lw + (b * kBatch + k) * kTpi + sub];
         dst[k] = row >= 0 && has
                      ? __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(row) * row_bytes) + piece)
                      : make_uint4(0u, 0u, 0u, 0u);
       }
     };
-    auto put = [&](uint32_t stage, int tk, int unit, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-      // unit: 8-channel group of the token's row
-      const uint32_t at = stage + (unit >> 3) * attn_tile::kPanelBytes + tk * 128 + (((unit & 7) ^ (tk & 7)) << 4);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+    constexpr int kX = kFp8 ? 8 : 16;  // words a piece expands to
+    auto put = [&](uint32_t stage, int tk, const uint32_t (&x)[kX]) {
+      if (!has) return;
+#pragma unroll
+      for (int u = 0; u < kX / 4; ++u) {
+        const int unit = kX / 4 * piece + u;  // 8-channel group of the token's row
+        const uint32_t at = stage + (unit >> 3) * attn_tile::kPanelBytes + tk * 128 + (((unit & 7) ^ (tk & 7)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[4 * u]), "r"(x[4 * u + 1]),
+                     "r"(x[4 * u + 2]), "r"(x[4 * u + 3])
+                     : "memory");
+      }
     };
 
     bool bad_now = false, bad_next = false;
-    int row_next;
     {
-      const int row = lookup(bad_now);
+      look();
+      const int row = found(bad_now);
       run.next_chunk(p);
-      row_next = lookup(bad_next);
-      s_rows[0][tid] = row;
+      look();
+      if (my_kv == 0) s_rows[0][my_tok] = row;
       load_scales(row);
       publish(0, bad_now);
       ok = attn_load_sync(true);
@@ -658,18 +683,18 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     for (int64_t c64 = 0; ok && c64 < total; ++c64) {
       const uint32_t c = static_cast<uint32_t>(c64);
       const int par = c & 1;
-      // rows of the next chunk, the lookups of the one after
-      s_rows[par ^ 1][tid] = row_next;
+      // rows and scales of the next chunk, the table's entries of the one after
+      const int row_next = found(bad_next);
+      if (my_kv == 0) s_rows[par ^ 1][my_tok] = row_next;
       load_scales(row_next);
-      const bool bad_pub = bad_next;
       run.next_chunk(p);
-      int row_after = lookup(bad_next);
+      look();
       if (!(ok = attn_load_sync(ok))) break;
 
       const int top = max(max(s_top[par][0], s_top[par][1]), max(s_top[par][2], s_top[par][3]));
       AttnNote& note = notes[c % attn_tile::kInfo];
       if (tid == 0) note.kfac = attn_scale_value(top);
-      if (bad_now) note.any = 1;
+      if (bad_now && my_kv == 0) note.any = 1;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++el) {
         const uint32_t sidx = el % kStages;
@@ -680,12 +705,13 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
           constexpr int kSeq = 2 * kNB;
           const int e = kv * kNB + b;
           uint4(&src)[kBatch] = buf[e & 1];
+          uint32_t nan = 0u;  // some byte's bit 7: a NaN among the batch's V codes
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
-            const int tk = 32 * lw + (b * kBatch + k) * kTpi + sub;
+            const int tk = 16 * lw + (b * kBatch + k) * kTpi + sub;
             const uint32_t w[4] = {src[k].x, src[k].y, src[k].z, src[k].w};
             const uint32_t sb = has ? s_scale[par][kv][tk][pblk] : 0u;
-            uint32_t x[kFp8 ? 8 : 16];
+            uint32_t x[kX];
             if (kv == 0) {
               const uint32_t f = sb == 255u ? 0x7E007E00u : attn_f16_pow2(top - static_cast<int>(sb));
 #pragma unroll
@@ -696,10 +722,10 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
                   attn_e2m1_f16(w[q], reinterpret_cast<uint32_t(&)[4]>(x[4 * q]));
               }
 #pragma unroll
-              for (int q = 0; q < (kFp8 ? 8 : 16); ++q) x[q] = attn_mul_f16x2(x[q], f);
+              for (int q = 0; q < kX; ++q) x[q] = attn_mul_f16x2(x[q], f);
             } else {
               const uint32_t f = attn_scale_pair<kFp8>(sb);
-              uint32_t nan = 0u;
+              if ((f & 0x7FFFu) == 0x7FFFu) nan = 0x80u;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (kFp8) {
@@ -712,26 +738,36 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
                     x[4 * q + h] = attn_mul_bf16x2(attn_e2m1_bits(w[q] << (12 - 4 * h)), f);
                 }
               }
-              if ((nan & 0x80808080u) != 0u || (f & 0x7FFFu) == 0x7FFFu) {
-                const bool all = (f & 0x7FFFu) == 0x7FFFu;
+            }
+            put(stage, tk, x);
+          }
+          if (kv == 1 && (nan & 0x80808080u) != 0u) {
+            // the rare way round: the pieces with a NaN again, with 0 in its place, and a note
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              const int tk = 16 * lw + (b * kBatch + k) * kTpi + sub;
+              const uint32_t w[4] = {src[k].x, src[k].y, src[k].z, src[k].w};
+              const uint32_t f = attn_scale_pair<kFp8>(has ? s_scale[par][1][tk][pblk] : 0u);
+              const bool all = (f & 0x7FFFu) == 0x7FFFu;
+              uint32_t x[kX], any = 0u;
+#pragma unroll
+              for (int q = 0; q < kX; ++q) x[q] = 0u;
+              if (kFp8 && !all) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                  const uint32_t z = kFp8 ? attn_e4m3_nan(w[q]) : 0u;
-                  if (kFp8) {
-                    x[2 * q] &= (z & 0x80u ? 0u : 0xFFFFu) | (z & 0x800000u ? 0u : 0xFFFF0000u);
-                    x[2 * q + 1] &= (z & 0x8000u ? 0u : 0xFFFFu) | (z & 0x80000000u ? 0u : 0xFFFF0000u);
-                  }
+                  const uint32_t z = attn_e4m3_nan(w[q]) & 0x80808080u;
+                  any |= z;
+                  x[2 * q] = attn_mul_bf16x2(attn_e4m3_bits(w[q] << 8), f) &
+                             ((z & 0x80u ? 0u : 0xFFFFu) | (z & 0x800000u ? 0u : 0xFFFF0000u));
+                  x[2 * q + 1] = attn_mul_bf16x2(attn_e4m3_bits(w[q]), f) &
+                                 ((z & 0x8000u ? 0u : 0xFFFFu) | (z & 0x80000000u ? 0u : 0xFFFF0000u));
                 }
-#pragma unroll
-                for (int q = 0; q < (kFp8 ? 8 : 16); ++q) x[q] = all ? 0u : x[q];
+              }
+              if (any != 0u || all) {
+                put(stage, tk, x);
                 atomicOr(&note.tok[tk], 1u << pblk);
                 note.any = 1;
               }
-            }
-            if (has) {
-#pragma unroll
-              for (int u = 0; u < (kFp8 ? 2 : 4); ++u)
-                put(stage, tk, (kFp8 ? 2 : 4) * piece + u, x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
             }
           }
           // the batch two steps on
@@ -743,82 +779,93 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
         __syncwarp();
         if (lane == 0) mbar_arrive(full(sidx));
       }
-      publish(c + 1, bad_pub);
-      bad_now = bad_pub;
-      row_next = row_after;
+      publish(c + 1, bad_next);
+      bad_now = bad_next;
       if (!(ok = attn_load_sync(ok))) break;
     }
   } else {
     // ================================================================ MMA
     setmaxnreg_dec<attn_tile::kRegsMma>();
-    if (warp == 12 && lane == 0) {
-      const uint32_t id_s = attn_idesc<false, false>(128), id_o = attn_idesc<true, true>(p.D);
-      const int ksteps = p.D / 16;
-      uint32_t el = 0;             // tiles taken from the ring
-      uint32_t n_q[2] = {0u, 0u}, n_p[2] = {0u, 0u};
-      bool ok = true;
-      auto issue_s = [&](int t, uint32_t stage) {
+    // the whole warp walks the runs and waits; one elected lane issues
+    if (warp == 16) {
+    const uint32_t id_s = attn_idesc<false, false>(128), id_o = attn_idesc<true, true>(p.D);
+    const int ksteps = p.D / 16;
+    uint32_t el = 0;             // tiles taken from the ring
+    uint32_t n_q[2] = {0u, 0u}, n_p[2] = {0u, 0u};
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t parity, unsigned int code) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, code));
+    };
+    auto issue_s = [&](int t, uint32_t stage) {
+      tc_fence_after();
+      if (attn_elect()) {
         const uint64_t a = smem_desc(q_base + t * C::kPanels * attn_tile::kPanelBytes, 16, 1024, 2);
         const uint64_t b = smem_desc(st_base + stage * C::kStageBytes, 16, 1024, 2);
-        for (int k = 0; k < ksteps; ++k) {
+#pragma unroll
+        for (int k = 0; k < kDP / 16; ++k) {
           const uint64_t off = ((k >> 2) * attn_tile::kPanelBytes + (k & 3) * 32) >> 4;
-          attn_mma_ss(s_col(t), a + off, b + off, id_s, k > 0);
+          if (k < ksteps) attn_mma_ss(s_col(t), a + off, b + off, id_s, k > 0);
         }
         tc_commit(s_full(t));
-      };
-      while (ok && run.left > 0) {
-        const int n = run.chunks_here();
-        const int tiles = C::kTiles == 1 ? 1 : run.tiles(p);
-        // first chunk's scores
-        const uint32_t k0 = el % kStages;
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint32_t bar) {
+      if (attn_elect()) tc_commit(bar);
+      __syncwarp();
+    };
+    while (ok && run.left > 0) {
+      const int n = run.chunks_here();
+      const int tiles = C::kTiles == 1 ? 1 : run.tiles(p);
+      // first chunk's scores
+      const uint32_t k0 = el % kStages;
+      for (int t = 0; ok && t < tiles; ++t) {
+        wait(q_full(t), n_q[t]++ & 1u, kErrWaitFull);
+        if (t == 0) wait(full(k0), (el / kStages) & 1u, kErrWaitFull);
+        if (ok) issue_s(t, k0);
+      }
+      if (!ok) break;
+      commit(empty(k0));
+      ++el;
+      for (int i = 0; ok && i < n; ++i) {
+        const uint32_t vst = el % kStages, vph = (el / kStages) & 1u;
+        const uint32_t kst = (el + 1) % kStages, kph = ((el + 1) / kStages) & 1u;
+        const bool more = i + 1 < n;
         for (int t = 0; ok && t < tiles; ++t) {
-          ok = mbar_wait(q_full(t), n_q[t]++ & 1u, kErrWaitFull);
-          if (ok && t == 0) ok = mbar_wait(full(k0), (el / kStages) & 1u, kErrWaitFull);
+          if (t == 0) wait(full(vst), vph, kErrWaitFull);
+          wait(p_full(t), n_p[t]++ & 1u, kErrWaitTmemEmpty);
           if (!ok) break;
           tc_fence_after();
-          issue_s(t, k0);
-        }
-        if (!ok) break;
-        tc_commit(empty(k0));
-        ++el;
-        for (int i = 0; ok && i < n; ++i) {
-          const uint32_t vst = el % kStages, vph = (el / kStages) & 1u;
-          const uint32_t kst = (el + 1) % kStages, kph = ((el + 1) / kStages) & 1u;
-          const bool more = i + 1 < n;
-          for (int t = 0; t < tiles; ++t) {
-            if (t == 0) ok = mbar_wait(full(vst), vph, kErrWaitFull);
-            ok = ok && mbar_wait(p_full(t), n_p[t]++ & 1u, kErrWaitTmemEmpty);
-            if (!ok) break;
-            tc_fence_after();
+          if (attn_elect()) {
             const uint64_t b = smem_desc(st_base + vst * C::kStageBytes, attn_tile::kPanelBytes, 1024, 2);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               attn_mma_ts(o_col(t), s_col(t) + 8 * k, b + ((k * 2048) >> 4), id_o, i > 0 || k > 0);
             tc_commit(o_full(t));
-            if (more) {
-              if (t == 0) ok = mbar_wait(full(kst), kph, kErrWaitFull);
-              if (!ok) break;
-              tc_fence_after();
-              issue_s(t, kst);
-            }
           }
-          if (!ok) break;
-          tc_commit(empty(vst));
-          if (more) tc_commit(empty(kst));
-          el += more ? 2 : 1;
+          __syncwarp();
+          if (more) {
+            if (t == 0) wait(full(kst), kph, kErrWaitFull);
+            if (ok) issue_s(t, kst);
+          }
         }
-        run.next_unit(p, n);
+        if (!ok) break;
+        commit(empty(vst));
+        if (more) commit(empty(kst));
+        el += more ? 2 : 1;
       }
-      // all MMAs done before TMEM is freed and the CTA's shared memory goes
-      tc_commit(drain);
-      mbar_wait(drain, 0, kErrWaitTmemFull);
+      run.next_unit(p, n);
     }
+    // all MMAs done before TMEM is freed and the CTA's shared memory goes
+    commit(drain);
+    mbar_wait(drain, 0, kErrWaitTmemFull);
     __syncwarp();
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace bat
