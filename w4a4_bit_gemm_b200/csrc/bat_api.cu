@@ -705,23 +705,24 @@ bat_status_t launch_dependent(Kernel k, dim3 grid, dim3 block, size_t smem, cuda
   return cuda_status(cudaLaunchKernelEx(&cfg, k, args...));
 }
 
-size_t attn_rows_smem(int nb4, int nt, int nb, bool qf, bool of) {
-  const size_t r = 8 * nt, dp = 128 * nb4;
-  size_t f = bat::attn::kWarps * r * (dp + 4) + bat::attn::kWarps * r * 2 + r * 2 + r * dp / 2 + r;
-  if (qf || of) f += bat::kv::kFacFloats;
-  f += static_cast<size_t>(nb) * 1024 * ((qf ? 1 : 0) + (of ? 1 : 0));
-  return f * 4;
+template <bool kFp8, int kNB, int kNT>
+size_t attn_rows_smem(size_t factor_floats) {
+  constexpr size_t r = 8 * kNT, dp = 32 * kNB;
+  using C = bat::AttnRowCfg<kFp8, kNB>;
+  return bat::attn_rows_ring_bytes(C::kWarpBytes, kNT, kNB) +
+         (bat::attn::kWarps * r * 2 + r * 2 + r * (dp + 4) + r + factor_floats) * 4 + r * dp * 2;
 }
 
-template <bool kFp8, int kNB4, int kNT>
+template <bool kFp8, int kNB, int kNT>
 bat_status_t launch_attn_rows(bat::AttnParams& p, int dev, int sms, int bit, cudaStream_t s) {
-  auto k = bat::bat_attn_rows_kernel<kFp8, kNB4, kNT>;
-  const size_t smem = attn_rows_smem(kNB4, kNT, p.nb, p.qa != nullptr, p.oa != nullptr);
-  bat_status_t st = attn_smem(k, dev, bit, attn_rows_smem(kNB4, kNT, 4 * kNB4, true, true));
+  auto k = bat::bat_attn_rows_kernel<kFp8, kNB, kNT>;
+  const size_t smem = attn_rows_smem<kFp8, kNB, kNT>((p.qa ? bat::attn_factor_floats(p.nb, p.qls) : 0) +
+                                                     (p.oa ? bat::attn_factor_floats(p.nb, p.ols) : 0));
+  bat_status_t st = attn_smem(k, dev, bit, attn_rows_smem<kFp8, kNB, kNT>(2 * bat::kv::kFacFloats));
   if (st != BAT_OK) return st;
   // two CTAs an SM where registers and shared memory allow; a few chunks need fewer CTAs,
   // but how many there are is known on the device only
-  const int per_sm = kNB4 == 1 && kNT == 1 && smem <= 110 * 1024 ? 2 : 1;
+  const int per_sm = kNB * kNT <= 4 && smem <= 112 * 1024 ? 2 : 1;
   p.ctas = per_sm * sms < kAttnRowCtas ? per_sm * sms : kAttnRowCtas;
   k<<<p.ctas, bat::attn::kThreads, smem, s>>>(p);
   return cuda_status(cudaGetLastError());
@@ -731,8 +732,8 @@ template <int kTile>
 bat_status_t launch_attn_join(const bat::AttnParams& p, int dev, int bit, cudaStream_t s) {
   if (p.ctas < 2) return BAT_OK;
   auto k = bat::bat_attn_join_kernel<kTile>;
-  const size_t max_smem = (8 * 260 + bat::kv::kFacFloats + 8 * 1024) * 4;
-  const size_t smem = (8 * 260 + (p.oa ? bat::kv::kFacFloats + p.nb * 1024 : 0)) * 4;
+  const size_t max_smem = (8 * 260 + bat::kv::kFacFloats) * 4;
+  const size_t smem = (8 * 260 + (p.oa ? bat::attn_factor_floats(p.nb, p.ols) : 0)) * 4;
   bat_status_t st = attn_smem(k, dev, bit, max_smem);
   if (st != BAT_OK) return st;
   return launch_dependent(k, dim3(p.ctas - 1, p.unit_rows / 8), dim3(256), smem, s, p);
@@ -1191,6 +1192,7 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   p.ols = ols;
   p.window = static_cast<int>(window < kMaxRows ? window : kMaxRows);
   p.sinks = static_cast<int>(sinks < kMaxRows ? sinks : kMaxRows);
+  p.scale_words = p.nb % 4 == 0 && ((reinterpret_cast<uintptr_t>(K->scales) | reinterpret_cast<uintptr_t>(V->scales)) & 3u) == 0;
   p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
   p.q_sign = scale < 0.0f ? -1.0f : 1.0f;
   const bool fp8 = K->fmt == BAT_KV_MXFP8;
@@ -1217,12 +1219,17 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
       return fp8 ? launch_attn_tile<true, 128>(p, dev, sms, 11, s) : launch_attn_tile<false, 128>(p, dev, sms, 12, s);
     return fp8 ? launch_attn_tile<true, 64>(p, dev, sms, 13, s) : launch_attn_tile<false, 64>(p, dev, sms, 14, s);
   }
+  // variants by the head's blocks (2, 4 or 8) and the unit's rows (8 or 16)
   if (D > 128)
-    st = fp8 ? launch_attn_rows<true, 2, 1>(p, dev, sms, 0, s) : launch_attn_rows<false, 2, 1>(p, dev, sms, 1, s);
+    st = fp8 ? launch_attn_rows<true, 8, 1>(p, dev, sms, 0, s) : launch_attn_rows<false, 8, 1>(p, dev, sms, 1, s);
+  else if (D > 64 && unit == 16)
+    st = fp8 ? launch_attn_rows<true, 4, 2>(p, dev, sms, 2, s) : launch_attn_rows<false, 4, 2>(p, dev, sms, 3, s);
+  else if (D > 64)
+    st = fp8 ? launch_attn_rows<true, 4, 1>(p, dev, sms, 4, s) : launch_attn_rows<false, 4, 1>(p, dev, sms, 5, s);
   else if (unit == 16)
-    st = fp8 ? launch_attn_rows<true, 1, 2>(p, dev, sms, 2, s) : launch_attn_rows<false, 1, 2>(p, dev, sms, 3, s);
+    st = fp8 ? launch_attn_rows<true, 2, 2>(p, dev, sms, 15, s) : launch_attn_rows<false, 2, 2>(p, dev, sms, 16, s);
   else
-    st = fp8 ? launch_attn_rows<true, 1, 1>(p, dev, sms, 4, s) : launch_attn_rows<false, 1, 1>(p, dev, sms, 5, s);
+    st = fp8 ? launch_attn_rows<true, 2, 1>(p, dev, sms, 17, s) : launch_attn_rows<false, 2, 1>(p, dev, sms, 18, s);
   if (st != BAT_OK) return st;
   return launch_attn_join<0>(p, dev, 6, s);
 }

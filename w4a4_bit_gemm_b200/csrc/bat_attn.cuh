@@ -65,7 +65,7 @@ struct AttnParams {
   const float* ob;
   uint16_t* out;           // bf16 [T][Hq][D]
   float* lse;              // fp32 [T][Hq] or null
-  float* part_o;           // [2 * ctas][rows][D]
+  float* part_o;           // [2 * ctas][rows][D], unnormalised
   float* part_ml;          // [2 * ctas][rows][2]
   AttnMark* marks;         // [ctas]
   int64_t T, num_slots;
@@ -79,6 +79,7 @@ struct AttnParams {
   int ctas;                // CTAs the chunks are dealt over
   int unit_rows;           // query rows of a unit
   int head_units;          // row kernel: units a token (Hkv * groups of rows); tile kernel: Hkv
+  int scale_words;         // the scale arrays may be read by 32-bit words (nb % 4 == 0, aligned)
   float scale_log2;        // |scale| * log2(e)
   float q_sign;            // sign of the scale, taken into q
   const uint16_t* qt;      // tile kernel with P_q: f16 rows of q P_q (attn_q_rows), or null
@@ -159,24 +160,39 @@ __device__ __forceinline__ int64_t attn_warp_scan(int64_t v, int lane) {
   return v;
 }
 
-// Chunks of all sequences (one warp, together).
-template <int kTile>
-__device__ __forceinline__ int64_t attn_total(const AttnParams& p, int lane) {
-  int64_t sum = 0;
-  for (int b = lane; b < p.B; b += 32) sum += attn_seq_chunks<kTile>(p, attn_seq(p, b));
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  return sum;
-}
+// The first chunk of CTA i's run: total / ctas chunks each, the remainder spread (ctas < 2^15).
+struct AttnDeal {
+  int64_t per;
+  uint32_t rem, ctas;
+  __device__ __forceinline__ AttnDeal(int64_t total, int n) {
+    ctas = static_cast<uint32_t>(n);
+    per = total < (int64_t{1} << 31) ? static_cast<int64_t>(static_cast<uint32_t>(total) / ctas) : total / n;
+    rem = static_cast<uint32_t>(total - per * n);
+  }
+  __device__ __forceinline__ int64_t start(int i) const { return per * i + rem * static_cast<uint32_t>(i) / ctas; }
+};
 
-// The place of chunk x, 0 <= x < total (one warp, together; every lane gets it).
+// The chunks of all sequences, and the place of the first chunk of CTA i's run (one warp,
+// together; every lane gets it).
 template <int kTile>
-__device__ __forceinline__ AttnPlace attn_locate(const AttnParams& p, int64_t x, int lane) {
-  AttnPlace pl;
-  pl.b = 0;
+__device__ __forceinline__ AttnMark attn_mark(const AttnParams& p, int cta, int lane, int64_t& run) {
+  AttnMark mk;
+  const int64_t w0 = lane < p.B ? attn_seq_chunks<kTile>(p, attn_seq(p, lane)) : 0;
+  int64_t total = w0;
+  for (int b = lane + 32; b < p.B; b += 32) total += attn_seq_chunks<kTile>(p, attn_seq(p, b));
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  const AttnDeal deal(total, p.ctas);
+  int64_t x = deal.start(cta);
+  run = deal.start(cta + 1) - x;
+  mk.x = x;
+  mk.total = total;
+  mk.place = AttnPlace{};
+  if (x >= total) return mk;
+  AttnPlace& pl = mk.place;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     const int b = b0 + lane;
-    const int64_t w = b < p.B ? attn_seq_chunks<kTile>(p, attn_seq(p, b)) : 0;
+    const int64_t w = b0 == 0 ? w0 : (b < p.B ? attn_seq_chunks<kTile>(p, attn_seq(p, b)) : 0);
     const int64_t inc = attn_warp_scan(w, lane);
     const int64_t all = __shfl_sync(0xffffffffu, inc, 31);
     if (x < all) {
@@ -190,8 +206,6 @@ __device__ __forceinline__ AttnPlace attn_locate(const AttnParams& p, int64_t x,
   }
   const AttnSeq s = attn_seq(p, pl.b);
   const int nt = attn_tiles<kTile>(p, s);
-  pl.tile = 0;
-  pl.chunks = 1;
   for (int t0 = 0; t0 < nt; t0 += 32) {
     const int t = t0 + lane;
     const int c = t < nt ? attn_chunks<kTile>(p, s, t) : 0;
@@ -208,14 +222,10 @@ __device__ __forceinline__ AttnPlace attn_locate(const AttnParams& p, int64_t x,
     }
     x -= all;
   }
-  pl.hu = static_cast<int>(x / pl.chunks);
-  pl.chunk = static_cast<int>(x % pl.chunks);
-  return pl;
-}
-
-// The first chunk of CTA i's run.
-__device__ __forceinline__ int64_t attn_start(int64_t total, int i, int ctas) {
-  return total / ctas * i + (total % ctas) * i / ctas;
+  // x < head_units * chunks < 2^31 (at most 2^30 rows of the cache are seen once by each head)
+  pl.hu = static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(pl.chunks));
+  pl.chunk = static_cast<int>(x) - pl.hu * pl.chunks;
+  return mk;
 }
 
 // The unit after (b, tile, hu) that exists.
@@ -257,12 +267,13 @@ __device__ __forceinline__ float attn_exp2(float x) {
 }
 
 // ---------------------------------------------------------------- stored elements -> f16, bf16
-// K's products run in f16: a conversion instruction gives two codes exactly, q (P_q) keeps 11
-// significant bits instead of bf16's 8, and f16's narrow range is no limit since both sides
-// are scaled by powers of two: a row of q by its largest channel, the K values by the largest MX
-// scale of their token (row kernel) or chunk (tile kernel). What falls below f16's range is
-// below 2^-25 of the largest products in the sum it belongs to. V cannot be scaled that way (its
-// channels and tokens are not summed with one maximum), so it goes to bf16, whose range is fp32's.
+// f16 takes two codes from one conversion instruction, exactly, and gives q P_q and the weights 11
+// significant bits instead of bf16's 8. Its narrow range is no limit where both sides of a sum
+// are scaled by powers of two: a row of q by its largest channel; in the row kernel the scores of
+// each 32-channel block by its MX scale in fp32, and V through the weights (below); in the
+// tile kernel K by the largest scale of its chunk, so that what falls below f16's range is below
+// 2^-25 of the chunk's largest products. The tile kernel's V goes to bf16, whose range is
+// fp32's: there the weights cannot take its scales up.
 __device__ __forceinline__ uint32_t attn_mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -303,6 +314,7 @@ __device__ __forceinline__ uint32_t attn_pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8) on the warp, f16 operands.
 __device__ __forceinline__ void attn_mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -335,22 +347,6 @@ __device__ __forceinline__ uint32_t attn_e2m1_bits(uint32_t x) {
 }
 // Bit 7 of a byte set where the E4M3 byte of w is a NaN (each magnitude is below 128).
 __device__ __forceinline__ uint32_t attn_e4m3_nan(uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; }
-// The pairs of attn_e4m3_bits with NaN put in for the NaN codes.
-__device__ __forceinline__ uint32_t attn_nan_pair(uint32_t r) {
-  if ((r & 0x7FFFu) == 0x07F0u) r |= 0x7FFFu;
-  if ((r & 0x7FFF0000u) == 0x07F00000u) r |= 0x7FFF0000u;
-  return r;
-}
-
-// D (16 x 8, fp32) += A (16 x 16, bf16) B (16 x 8, bf16) on the warp.
-__device__ __forceinline__ void attn_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ uint32_t attn_transpose8(uint32_t x) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -361,39 +357,51 @@ __device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Rows' results from unnormalised sums in shared memory: o[r * ldo + d] (in units of 2^-32),
-// ml[2 r] the maximum, ml[2 r + 1] the sum. P_o (po, null: none) is applied to the normalised
-// fp32 values, and the output is rounded to bf16 once. (token, head) of row r from `where`.
-template <class Where>
-__device__ __forceinline__ void attn_finish(const AttnParams& p, const float* o, int ldo, const float* ml,
-                                            int rows, const float* po, Where where) {
-  const int pairs = p.D >> 1;
-  for (int i = threadIdx.x; i < rows * pairs; i += blockDim.x) {
-    const int r = i / pairs, d = 2 * (i - r * pairs);
-    int64_t tok;
-    int head;
-    if (!where(r, tok, head)) continue;
-    const float l = ml[2 * r + 1];
-    const float inv = l > 0.0f ? attn::kUp / l : (l == 0.0f ? 0.0f : l);  // l NaN stays NaN
-    float v0, v1;
-    if (po == nullptr) {
-      v0 = o[r * ldo + d] * inv;
-      v1 = o[r * ldo + d + 1] * inv;
-    } else {
-      const float* src = o + r * ldo + (d & ~31);
-      const float* pb = po + (d >> 5) * 1024 + (d & 31);
-      v0 = v1 = 0.0f;
-#pragma unroll 8
-      for (int k = 0; k < 32; ++k) {
-        const float x = src[k] * inv;
-        const float2 c = *reinterpret_cast<const float2*>(pb + 32 * k);
-        v0 = __fmaf_rn(x, c.x, v0);
-        v1 = __fmaf_rn(x, c.y, v1);
-      }
+// ---------------------------------------------------------------- block transforms
+// Factors of P staged in shared memory: A, then B (when they fit; else read where they are).
+struct AttnFactors {
+  const float* a;
+  const float* b;
+  int ls;
+};
+__host__ __device__ constexpr int attn_factor_floats(int nb, int ls) {
+  const int na = 1 << (2 * ls), nbf = nb << (10 - 2 * ls);
+  return (na + 3) / 4 * 4 + nbf <= kv::kFacFloats ? (na + 3) / 4 * 4 + (nbf + 3) / 4 * 4 : 0;
+}
+// (no barrier: the caller's next one orders it)
+__device__ __forceinline__ AttnFactors attn_stage_factors(float* dst, const float* a, const float* b, int nb, int ls) {
+  if (attn_factor_floats(nb, ls) == 0) return AttnFactors{a, b, ls};
+  const int na = 1 << (2 * ls), nbf = nb << (10 - 2 * ls);
+  float* db = dst + (na + 3) / 4 * 4;
+  for (int i = threadIdx.x; i < na; i += blockDim.x) dst[i] = __ldg(a + i);
+  for (int i = threadIdx.x; i < nbf; i += blockDim.x) db[i] = __ldg(b + i);
+  return AttnFactors{dst, db, ls};
+}
+// The four outputs n = q, 8 + q, 16 + q, 24 + q (q < 8) of block `blk`: y = x (B_blk (x) A), x the
+// block's 32 values. The 8 x 8 / 4 x 4 split goes by its two small products.
+__device__ __forceinline__ void attn_block_apply(const AttnFactors& f, int blk, const float* x, int q, float (&y)[4]) {
+  if (f.ls == 3) {
+    y[0] = y[1] = y[2] = y[3] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float z = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) z = __fmaf_rn(x[8 * i + k], f.a[8 * k + q], z);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = __fmaf_rn(z, f.b[16 * blk + 4 * i + j], y[j]);
     }
-    *reinterpret_cast<uint32_t*>(p.out + (tok * p.Hq + head) * p.D + d) = attn_pack(v0, v1);
-    if (p.lse && d == 0)
-      p.lse[tok * p.Hq + head] = l == 0.0f ? -INFINITY : (ml[2 * r] + log2f(l)) * 0.69314718055994531f;
+    return;
+  }
+  const int sm = (1 << f.ls) - 1, t = 32 >> f.ls;
+  const float* bb = f.b + static_cast<int64_t>(blk) * t * t;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = 8 * j + q;
+    float acc = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < 32; ++k)
+      acc = __fmaf_rn(x[k], __fmul_rn(bb[(k >> f.ls) * t + (n >> f.ls)], f.a[((k & sm) << f.ls) + (n & sm)]), acc);
+    y[j] = acc;
   }
 }
 
@@ -401,72 +409,88 @@ __device__ __forceinline__ void attn_finish(const AttnParams& p, const float* o,
 // A unit is one token and up to 8 kNT of its heads that share a KV head; a warp takes 16 of
 // the chunk's 128 tokens, keeps its own running maximum, sum and o, and the eight warps join
 // at the unit's end. Products on mma.sync with the tokens on the 16-row side,
-//   S^T = K q^T (16 tokens x 8 heads),   o^T += V^T P^T (D x 16 tokens),
-// so that 8 heads fill the other side; both contractions may run over permuted indices, and
-// the order is chosen so that each lane's operands are its own 16-byte loads of stored
-// codes: lane 4 r + c holds channels of block c (and c + 4) of tokens r and r + 8 for K, and 1/8
-// of the channels of tokens 2c, 2c+1, 2c+8, 2c+9 for V. Codes go from global memory to
-// registers to the MMA; nothing is staged in shared memory. All rows of a unit see the
-// same tokens, so a masked token is simply not loaded (its weight and value are 0).
-// Bound: HBM; a CTA has 32 KB of MXFP8 codes in flight, two CTAs an SM.
-template <bool kFp8, int kNB4>
-struct AttnRowRegs {
-  static constexpr int kKw = kFp8 ? 8 : 4;           // K words a token and block
-  static constexpr int kVw = (kFp8 ? 4 : 2) * kNB4;  // V words a token
-  uint32_t k[2][kNB4][kKw];
-  uint32_t v[4][kVw];
-  uint32_t ks[2][kNB4];  // scale bytes
-  uint32_t vs[4];
+//   S^T = K q^T (16 tokens x 8 heads),   o^T += V^T P^T (channels x 16 tokens),
+// so that 8 heads fill the other side. All rows of a unit see the same tokens, so a masked token is
+// simply not loaded (zeros in its place).
+// Each warp streams its tokens through its own ring in shared memory (16-byte asynchronous
+// copies, kStages tiles of K and of V in flight, refilled as soon as a tile is used), so no
+// barrier is met between a unit's start and its end, and the loads' latency is covered whatever
+// the lengths (loads to registers one tile ahead: 2.0-2.5 us a chunk where this takes 1.0-1.4).
+// Scales: S^T of each 32-channel block is multiplied by the tokens' K scales in fp32. For V, with E
+// the largest scale exponent of a token, the weights are taken as
+//   w = 2^(x + E - M),  M the running maximum of x + E  (x: the score in log2 units),
+// and multiplied by 2^(e_b - E) <= 1 for block b, so V's codes enter the product as they are.
+// Bound: HBM bytes for KV8; about 300 instructions a warp and tile, near the issue limit, for KV4.
+template <bool kFp8, int kNB>
+struct AttnRowCfg {
+  static constexpr int kBytes = kFp8 ? 32 * kNB : 16 * kNB;  // codes of a token, padded to kNB blocks
+  // row strides in shared memory that keep the fragment loads free of bank conflicts: K is read
+  // by 8 bytes (E4M3) at 8 c of tokens r, by 4 (E2M1); V by 4 or 2 bytes of tokens 2c
+  static constexpr int kKs = kFp8 ? kBytes + 32 : kBytes + 16;
+  static constexpr int kVs = kBytes + 16;
+  static constexpr int kStages = kFp8 ? (kNB == 2 ? 3 : 2) : (kNB == 2 ? 4 : (kNB == 4 ? 3 : 2));
+  static constexpr int kStageBytes = 16 * (kKs + kVs);
+  // factors of a tile: K scales fp32 [16][kNB], V factors f16 [kNB][16], E fp32 [16]
+  static constexpr int kFacBytes = 16 * kNB * 4 + 16 * kNB * 2 + 64;
+  static constexpr int kWarpBytes = kStages * kStageBytes + 2 * kFacBytes;
 };
+constexpr size_t attn_rows_ring_bytes(int warp_bytes, int nt, int nb) {
+  const size_t ring = static_cast<size_t>(attn::kWarps) * warp_bytes;
+  const size_t join = static_cast<size_t>(attn::kWarps) * 8 * nt * (32 * nb + 4) * 4;  // takes the ring's place
+  return ring > join ? ring : join;
+}
 
-template <bool kFp8, int kNB4, int kNT>
-__global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
-    bat_attn_rows_kernel(const AttnParams p) {
+__device__ __forceinline__ void attn_copy16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void attn_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void attn_copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+template <bool kFp8, int kNB, int kNT>
+__global__ void __launch_bounds__(attn::kThreads, kNB * kNT <= 4 ? 2 : 1) bat_attn_rows_kernel(const AttnParams p) {
+  using C = AttnRowCfg<kFp8, kNB>;
   extern __shared__ __align__(16) float smem[];
-  constexpr int kDP = 128 * kNB4, kR = 8 * kNT;
-  constexpr int kKw = kFp8 ? 8 : 4, kVw = (kFp8 ? 4 : 2) * kNB4;
-  constexpr int kMT = kDP / 16;  // m16 tiles of o^T
-  // shared memory: [warps][kR][kDP + 4] o, [warps][kR][2] maximum and sum, q rows, P_q, P_o
+  constexpr int kDP = 32 * kNB, kR = 8 * kNT, kS = C::kStages;
   constexpr int kLdo = kDP + 4;
-  float* so = smem;
-  float* sml = so + attn::kWarps * kR * kLdo;
-  float* fml = sml + attn::kWarps * kR * 2;  // [kR][2]
-  uint16_t* sq = reinterpret_cast<uint16_t*>(fml + kR * 2);  // [kR][kDP] f16
-  float* sqf = reinterpret_cast<float*>(sq + kR * kDP);      // [kR] factors of the q rows
-  float* fac = sqf + kR;                                     // kFacFloats when factors are given
-  const bool any_fac = p.qa != nullptr || p.oa != nullptr;
-  float* pq = fac + (any_fac ? kv::kFacFloats : 0);
-  float* po = pq + (p.qa ? p.nb * 1024 : 0);
+  float* so = smem;  // the rings; at a unit's end [warps][kR][kLdo] o
+  float* sml = smem + attn_rows_ring_bytes(C::kWarpBytes, kNT, kNB) / 4;  // [warps][kR][2] maximum and sum
+  float* fml = sml + attn::kWarps * kR * 2;                    // [kR][2]
+  float* sy = fml + kR * 2;                                    // [kR][kLdo] q rows in fp32
+  float* sqf = sy + kR * kLdo;                                 // [kR] factors of the q rows
+  uint16_t* sq = reinterpret_cast<uint16_t*>(sqf + kR);        // [kR][kDP] f16
+  float* fac_q = reinterpret_cast<float*>(sq + kR * kDP);
+  float* fac_o = fac_q + (p.qa ? attn_factor_floats(p.nb, p.qls) : 0);
   __shared__ AttnPlace s_place;
-  __shared__ int64_t s_run[2];
+  __shared__ int64_t s_run;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane & 3, r = lane >> 2;
   allow_dependents();
   if (warp == 0) {
-    const int64_t total = attn_total<0>(p, lane);
-    const int64_t x0 = attn_start(total, blockIdx.x, p.ctas), x1 = attn_start(total, blockIdx.x + 1, p.ctas);
-    AttnPlace pl{};
-    if (x0 < total) pl = attn_locate<0>(p, x0, lane);
+    int64_t run;
+    const AttnMark mk = attn_mark<0>(p, blockIdx.x, lane, run);
     if (lane == 0) {
-      s_place = pl;
-      s_run[0] = x0;
-      s_run[1] = x1;
-      p.marks[blockIdx.x] = AttnMark{x0, total, pl};
+      s_place = mk.place;
+      s_run = run;
+      p.marks[blockIdx.x] = mk;
     }
   }
-  if (p.qa) kv_build_p(pq, fac, p.qa, p.qb, p.nb, p.qls);
-  if (p.oa) {
-    __syncthreads();
-    kv_build_p(po, fac, p.oa, p.ob, p.nb, p.ols);
-  }
+  AttnFactors fq{nullptr, nullptr, 3}, fo{nullptr, nullptr, 3};
+  if (p.qa) fq = attn_stage_factors(fac_q, p.qa, p.qb, p.nb, p.qls);
+  if (p.oa) fo = attn_stage_factors(fac_o, p.oa, p.ob, p.nb, p.ols);
   __syncthreads();
   AttnPlace pl = s_place;
-  int64_t left = s_run[1] - s_run[0];
+  int64_t left = s_run;
   if (left <= 0) return;
   AttnSeq seq = attn_seq(p, pl.b);
   const int hgs = p.head_units / p.Hkv;  // groups of kR heads of a KV head
   const int row_bytes = kFp8 ? p.D : p.D / 2;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(smem) + warp * C::kWarpBytes;
+  uint8_t* facs = ring + kS * C::kStageBytes;
+  const uint32_t ring32 = smem_u32(ring);
 
   for (int seg = 0; left > 0; ++seg) {
     const int h = pl.hu / hgs, hg = pl.hu - h * hgs;
@@ -479,39 +503,110 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
     const int last = static_cast<int>(min(static_cast<int64_t>(pl.chunks), first + left));  // chunks [first, last)
     const int32_t* pages = p.table + static_cast<int64_t>(pl.b) * p.max_pages;
 
-    // q rows (times P_q) in fp32, then in f16 with the row's power of two
-    for (int i = threadIdx.x; i < kR * (kDP / 2); i += attn::kThreads) {
-      const int n = i / (kDP / 2), d = 2 * (i - n * (kDP / 2));
-      float y0 = 0.0f, y1 = 0.0f;
-      if (n < nrows && d < p.D) {
-        const uint16_t* src = p.q + tok * p.q_stride + static_cast<int64_t>(head0 + n) * p.D;
-        if (p.qa == nullptr) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(src + d);
-          y0 = bf16lo(w);
-          y1 = bf16hi(w);
+    // ---- the warp's stream: token `lane & 15` of its tiles
+    int j_ahead, page_ahead = 0;
+    auto look = [&](int chunk) {
+      const int i = chunk * attn::kChunk + 16 * warp + (lane & 15);
+      j_ahead = chunk < last && i < nv ? span.token(i) : -1;
+      if (j_ahead >= 0) page_ahead = __ldg(pages + attn_page_of(p, j_ahead));
+    };
+    auto found = [&]() -> int { return j_ahead >= 0 ? attn_row_at(p, page_ahead, j_ahead, h) : -1; };
+    constexpr int kPieces = C::kBytes / 16;
+    auto copy = [&](int rows16, const uint8_t* codes, uint32_t dst, int stride) {
+#pragma unroll
+      for (int k = 0; k < 16 * kPieces / 32; ++k) {
+        const int tk = (32 * k + lane) / kPieces, piece = (32 * k + lane) % kPieces;
+        const int row = __shfl_sync(0xffffffffu, rows16, tk);
+        const bool ok = row >= 0 && 16 * piece < row_bytes;
+        attn_copy16(dst + tk * stride + 16 * piece, ok ? codes + static_cast<int64_t>(row) * row_bytes + 16 * piece : codes, ok);
+      }
+      attn_copy_commit();
+    };
+    auto copy_k = [&](int rows16, int st) { copy(rows16, p.k_codes, ring32 + st * C::kStageBytes, C::kKs); };
+    auto copy_v = [&](int rows16, int st) { copy(rows16, p.v_codes, ring32 + st * C::kStageBytes + 16 * C::kKs, C::kVs); };
+    // scale bytes of the lane's token: K's for lanes 0..15, V's for 16..31, four a word
+    uint32_t sc[(kNB + 3) / 4];
+    auto load_scales = [&](int row) {
+      const uint8_t* src = (lane < 16 ? p.k_scales : p.v_scales) + static_cast<int64_t>(row) * p.nb;
+#pragma unroll
+      for (int w = 0; w < (kNB + 3) / 4; ++w) {
+        sc[w] = 0u;
+        if (row < 0) continue;
+        if (p.scale_words) {
+          sc[w] = 4 * w < p.nb ? __ldg(reinterpret_cast<const uint32_t*>(src) + w) : 0u;
         } else {
-          const uint32_t* s2 = reinterpret_cast<const uint32_t*>(src + (d & ~31));
-          const float* pb = pq + (d >> 5) * 1024 + (d & 31);
-#pragma unroll 4
-          for (int k = 0; k < 16; ++k) {
-            const uint32_t x = s2[k];
-            const float2 c0 = *reinterpret_cast<const float2*>(pb + 64 * k);
-            const float2 c1 = *reinterpret_cast<const float2*>(pb + 64 * k + 32);
-            y0 = __fmaf_rn(bf16lo(x), c0.x, y0);
-            y1 = __fmaf_rn(bf16lo(x), c0.y, y1);
-            y0 = __fmaf_rn(bf16hi(x), c1.x, y0);
-            y1 = __fmaf_rn(bf16hi(x), c1.y, y1);
-          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (4 * w + k < p.nb) sc[w] |= static_cast<uint32_t>(__ldg(src + 4 * w + k)) << (8 * k);
         }
       }
-      *reinterpret_cast<float2*>(so + n * kLdo + d) = make_float2(y0, y1);
+    };
+    auto put_scales = [&](int par) {
+      float* fk = reinterpret_cast<float*>(facs + par * C::kFacBytes);
+      uint16_t* fv = reinterpret_cast<uint16_t*>(fk + 16 * kNB);
+      float* fe = reinterpret_cast<float*>(fv + 16 * kNB);
+      const int tk = lane & 15;
+      if (lane < 16) {
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) fk[tk * kNB + b] = attn_scale_value((sc[b / 4] >> (8 * (b & 3))) & 255u);
+      } else {
+        int top = 0;
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+          const int e = (sc[b / 4] >> (8 * (b & 3))) & 255u;
+          top = e != 255 ? max(top, e) : top;
+        }
+        // tokens 2c, 2c + 1, 2c + 8, 2c + 9 side by side
+        const int at = (tk & 6) * 2 + (tk & 1) + (tk >> 3) * 2;
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+          const int e = (sc[b / 4] >> (8 * (b & 3))) & 255u;
+          fv[b * 16 + at] = static_cast<uint16_t>(e == 255 ? 0x7E00u : attn_f16_pow2(top - e));
+        }
+        fe[tk] = static_cast<float>(top - 127);
+      }
+    };
+
+    int rw[kS + 1];  // cache rows of tiles i .. i + kS - 1 of the warp
+#pragma unroll
+    for (int k = 0; k < kS; ++k) {
+      look(first + k);
+      rw[k] = found();
+    }
+    load_scales(rw[0]);
+#pragma unroll
+    for (int k = 0; k < kS; ++k) {
+      copy_k(rw[k], k);
+      copy_v(rw[k], k);
+    }
+    look(first + kS);
+
+    // ---- q rows (times P_q) in fp32, then in f16 with the row's power of two
+    for (int i = threadIdx.x; i < kR * kNB * 8; i += attn::kThreads) {
+      const int q = i & 7, blk = (i >> 3) % kNB, n = (i >> 3) / kNB;
+      const bool has = n < nrows && blk < p.nb;
+      const uint16_t* src = p.q + tok * p.q_stride + static_cast<int64_t>(head0 + n) * p.D + 32 * blk;
+      float* dst = sy + n * kLdo + 32 * blk;
+      if (p.qa == nullptr) {
+        const uint2 w = has ? *reinterpret_cast<const uint2*>(src + 4 * q) : make_uint2(0u, 0u);
+        *reinterpret_cast<float4*>(dst + 4 * q) = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+      } else {
+        float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (has) {
+          float x[32];
+          rows_load_block(src, x);
+          attn_block_apply(fq, blk, x, q, y);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dst[8 * j + q] = y[j];
+      }
     }
     __syncthreads();
     for (int n = warp; n < kR; n += attn::kWarps) {
       float y[kDP / 32], mx = 0.0f;
 #pragma unroll
       for (int k = 0; k < kDP / 64; ++k) {
-        const float2 v = *reinterpret_cast<const float2*>(so + n * kLdo + 64 * k + 2 * lane);
+        const float2 v = *reinterpret_cast<const float2*>(sy + n * kLdo + 64 * k + 2 * lane);
         y[2 * k] = v.x;
         y[2 * k + 1] = v.y;
         mx = fmaxf(mx, fmaxf(fabsf(v.x), fabsf(v.y)));
@@ -526,301 +621,261 @@ __global__ void __launch_bounds__(attn::kThreads, kNB4 == 1 && kNT == 1 ? 2 : 1)
       if (lane == 0) sqf[n] = down * p.scale_log2;
     }
     __syncthreads();
-    // this lane's q operands: heads r (and r + 8), the channels of its K words; the factors
-    // of its score columns
-    uint32_t qf[kNT][kNB4][16];
+    // this lane's q operands: heads r (and r + 8), channels 8 c .. 8 c + 7 of every block; the
+    // factors of its score columns
+    uint32_t qf[kNT][kNB][4];
     float cs[kNT][2];
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
       cs[t][0] = sqf[8 * t + 2 * c];
       cs[t][1] = sqf[8 * t + 2 * c + 1];
 #pragma unroll
-      for (int b4 = 0; b4 < kNB4; ++b4) {
-        const uint4* src = reinterpret_cast<const uint4*>(sq + (8 * t + r) * kDP + 32 * (c + 4 * b4));
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const uint4 w = src[s];
-          qf[t][b4][4 * s] = w.x;
-          qf[t][b4][4 * s + 1] = w.y;
-          qf[t][b4][4 * s + 2] = w.z;
-          qf[t][b4][4 * s + 3] = w.w;
-        }
+      for (int b = 0; b < kNB; ++b) {
+        const uint4 w = *reinterpret_cast<const uint4*>(sq + (8 * t + r) * kDP + 32 * b + 8 * c);
+        qf[t][b][0] = w.x;
+        qf[t][b][1] = w.y;
+        qf[t][b][2] = w.z;
+        qf[t][b][3] = w.w;
       }
     }
+    put_scales(0);
+    load_scales(rw[1]);
 
-    float m[kNT][2], l[kNT][2], o[kNT][kMT][4];
+    // m, M: running references of the scores and of score + E (within 2^8 of the maxima)
+    float m[kNT][2], mv[kNT][2], l[kNT][2], o[kNT][2 * kNB][4];
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
-      m[t][0] = m[t][1] = -INFINITY;
+      m[t][0] = m[t][1] = mv[t][0] = mv[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
+      for (int i = 0; i < 2 * kNB; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
     }
 
-    // cache row of token `lane` of this warp's 16 (lanes 16..31 repeat), -1: none
-    auto lookup = [&](int chunk) -> int {
-      const int i = chunk * attn::kChunk + 16 * warp + (lane & 15);
-      if (chunk >= last || i >= nv) return -1;
-      return attn_cache_row(p, pages, span.token(i), h);
-    };
-    AttnRowRegs<kFp8, kNB4> g;
-    auto load_k = [&](int rows16) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int row = __shfl_sync(0xffffffffu, rows16, r + 8 * x);
-#pragma unroll
-        for (int b4 = 0; b4 < kNB4; ++b4) {
-          const int blk = c + 4 * b4;
-          const bool ok = row >= 0 && blk < p.nb;
-          const uint4* src = reinterpret_cast<const uint4*>(p.k_codes + static_cast<int64_t>(row) * row_bytes +
-                                                            blk * (kFp8 ? 32 : 16));
-#pragma unroll
-          for (int k = 0; k < kKw / 4; ++k) {
-            const uint4 w = ok ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-            g.k[x][b4][4 * k] = w.x;
-            g.k[x][b4][4 * k + 1] = w.y;
-            g.k[x][b4][4 * k + 2] = w.z;
-            g.k[x][b4][4 * k + 3] = w.w;
-          }
-          g.ks[x][b4] = ok ? __ldg(p.k_scales + static_cast<int64_t>(row) * p.nb + blk) : 0u;
-        }
-      }
-    };
-    const bool v_has = 16 * kNB4 * r < p.D;
-    auto load_v = [&](int rows16) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int row = __shfl_sync(0xffffffffu, rows16, 2 * c + (x & 1) + 8 * (x >> 1));
-        const bool ok = row >= 0 && v_has;
-        const uint8_t* src = p.v_codes + static_cast<int64_t>(row) * row_bytes + r * (kVw * 4);
-        if (kVw == 2) {
-          const uint2 w = ok ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0u, 0u);
-          g.v[x][0] = w.x;
-          g.v[x][1] = w.y;
-        } else {
-#pragma unroll
-          for (int k = 0; k < kVw / 4; ++k) {
-            const uint4 w = ok ? __ldg(reinterpret_cast<const uint4*>(src) + k) : make_uint4(0u, 0u, 0u, 0u);
-            g.v[x][4 * k] = w.x;
-            g.v[x][4 * k + 1] = w.y;
-            g.v[x][4 * k + 2] = w.z;
-            g.v[x][4 * k + 3] = w.w;
-          }
-        }
-        g.vs[x] = ok ? __ldg(p.v_scales + static_cast<int64_t>(row) * p.nb + (16 * kNB4 * r >> 5)) : 0u;
-      }
-    };
-
-    int rows_now = lookup(first);
-    load_k(rows_now);
-    load_v(rows_now);
-    int rows_next = lookup(first + 1);
+    int st = 0;
     for (int ch = first; ch < last; ++ch) {
-      // ---- S^T = K q^T
+      const int par = (ch - first) & 1;
+      rw[kS] = found();
+      look(ch + kS + 1);
+      put_scales(par ^ 1);
+      load_scales(rw[2]);
+      attn_copy_wait<2 * kS - 1>();
+      __syncwarp();
+      const uint8_t* kt = ring + st * C::kStageBytes;
+      const uint8_t* vt = kt + 16 * C::kKs;
+      const float* fk = reinterpret_cast<const float*>(facs + par * C::kFacBytes);
+      const uint16_t* fv = reinterpret_cast<const uint16_t*>(fk + 16 * kNB);
+      const float* fe = reinterpret_cast<const float*>(fv + 16 * kNB);
+      // ---- S^T = K q^T, a block at a time
       float s[kNT][4];
 #pragma unroll
       for (int t = 0; t < kNT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
-      int top[2];  // the tokens' largest scale bytes (the quad holds a token's blocks)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        top[x] = static_cast<int>(g.ks[x][0]);
-        if (kNB4 == 2) top[x] = max(top[x], static_cast<int>(g.ks[x][kNB4 - 1]));
-        top[x] = max(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
-        top[x] = max(top[x], __shfl_xor_sync(0xffffffffu, top[x], 2));
-      }
+      for (int b = 0; b < kNB; ++b) {
+        if (b >= p.nb) break;
+        uint32_t a[2][4];
 #pragma unroll
-      for (int b4 = 0; b4 < kNB4; ++b4) {
-        const uint32_t f0 = attn_f16_pow2(top[0] - static_cast<int>(g.ks[0][b4]));
-        const uint32_t f1 = attn_f16_pow2(top[1] - static_cast<int>(g.ks[1][b4]));
-#pragma unroll
-        for (int w = 0; w < kKw; ++w) {
-          // a word holds one k-step's (E4M3) or two k-steps' (E2M1) operands of this lane
-          uint32_t a[2][4];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (kFp8)
-              attn_e4m3_f16(g.k[x][b4][w], a[x][0], a[x][1]);
-            else
-              attn_e2m1_f16(g.k[x][b4][w], a[x]);
-#pragma unroll
-            for (int e = 0; e < (kFp8 ? 2 : 4); ++e) a[x][e] = attn_mul_f16x2(a[x][e], x ? f1 : f0);
-          }
-#pragma unroll
-          for (int e = 0; e < (kFp8 ? 2 : 4); e += 2) {
-            const int st = kFp8 ? w : 2 * w + e / 2;
-#pragma unroll
-            for (int t = 0; t < kNT; ++t)
-              attn_mma_f16(s[t], a[0][e], a[1][e], a[0][e + 1], a[1][e + 1], qf[t][b4][2 * st], qf[t][b4][2 * st + 1]);
+        for (int x = 0; x < 2; ++x) {
+          const uint8_t* src = kt + (r + 8 * x) * C::kKs;
+          if (kFp8) {
+            const uint2 w = *reinterpret_cast<const uint2*>(src + 32 * b + 8 * c);
+            attn_e4m3_f16(w.x, a[x][0], a[x][1]);
+            attn_e4m3_f16(w.y, a[x][2], a[x][3]);
+          } else {
+            attn_e2m1_f16(*reinterpret_cast<const uint32_t*>(src + 16 * b + 4 * c), a[x]);
           }
         }
+        const float k0 = fk[r * kNB + b], k1 = fk[(r + 8) * kNB + b];
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          attn_mma_f16(d, a[0][0], a[1][0], a[0][1], a[1][1], qf[t][b][0], qf[t][b][1]);
+          attn_mma_f16(d, a[0][2], a[1][2], a[0][3], a[1][3], qf[t][b][2], qf[t][b][3]);
+          s[t][0] = __fmaf_rn(d[0], k0, s[t][0]);
+          s[t][1] = __fmaf_rn(d[1], k0, s[t][1]);
+          s[t][2] = __fmaf_rn(d[2], k1, s[t][2]);
+          s[t][3] = __fmaf_rn(d[3], k1, s[t][3]);
+        }
       }
-      const float kv0 = attn_scale_value(top[0]), kv1 = attn_scale_value(top[1]);
-      const bool see0 = __shfl_sync(0xffffffffu, rows_now, r) >= 0;
-      const bool see1 = __shfl_sync(0xffffffffu, rows_now, r + 8) >= 0;
-      load_k(rows_next);
-      const int rows_after = lookup(ch + 2);
+      const bool see0 = __shfl_sync(0xffffffffu, rw[0], r) >= 0;
+      const bool see1 = __shfl_sync(0xffffffffu, rw[0], r + 8) >= 0;
+      const float e0 = fe[r], e1 = fe[r + 8];
+      __syncwarp();
+      copy_k(rw[kS], st);
       // ---- softmax over the tokens, for the columns 2c and 2c + 1
       uint32_t pb[kNT][2];
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
-        float x[4], mx[2];
-        x[0] = see0 ? s[t][0] * kv0 * cs[t][0] : -INFINITY;
-        x[1] = see0 ? s[t][1] * kv0 * cs[t][1] : -INFINITY;
-        x[2] = see1 ? s[t][2] * kv1 * cs[t][0] : -INFINITY;
-        x[3] = see1 ? s[t][3] * kv1 * cs[t][1] : -INFINITY;
-        mx[0] = fmaxf(x[0], x[2]);
-        mx[1] = fmaxf(x[1], x[3]);
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], d));
-          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], d));
-        }
-        const bool up = mx[0] > m[t][0] || mx[1] > m[t][1];
+        float x[4];
+        x[0] = see0 ? s[t][0] * cs[t][0] : -INFINITY;
+        x[1] = see0 ? s[t][1] * cs[t][1] : -INFINITY;
+        x[2] = see1 ? s[t][2] * cs[t][0] : -INFINITY;
+        x[3] = see1 ? s[t][3] * cs[t][1] : -INFINITY;
+        const float a0 = fmaxf(x[0], x[2]), a1 = fmaxf(x[1], x[3]);
+        const float b0 = fmaxf(x[0] + e0, x[2] + e1), b1 = fmaxf(x[1] + e0, x[3] + e1);
+        const bool up = a0 > m[t][0] + 8.0f || a1 > m[t][1] + 8.0f || b0 > mv[t][0] + 8.0f || b1 > mv[t][1] + 8.0f;
         if (__any_sync(0xffffffffu, up)) {
-          float al[2];
+          float nm[2] = {a0, a1}, nv2[2] = {b0, b1};
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float mn = fmaxf(m[t][k], mx[k]);
-            al[k] = mn == -INFINITY ? 1.0f : attn_exp2(m[t][k] - mn);
-            m[t][k] = mn;
-            l[t][k] *= al[k];
-          }
 #pragma unroll
-          for (int i = 0; i < kMT; ++i) {
-            o[t][i][0] *= al[0];
-            o[t][i][1] *= al[1];
-            o[t][i][2] *= al[0];
-            o[t][i][3] *= al[1];
+            for (int d = 4; d < 32; d <<= 1) {
+              nm[k] = fmaxf(nm[k], __shfl_xor_sync(0xffffffffu, nm[k], d));
+              nv2[k] = fmaxf(nv2[k], __shfl_xor_sync(0xffffffffu, nv2[k], d));
+            }
+            nm[k] = fmaxf(m[t][k], nm[k]);
+            nv2[k] = fmaxf(mv[t][k], nv2[k]);
+            l[t][k] *= nm[k] == -INFINITY ? 1.0f : attn_exp2(m[t][k] - nm[k]);
+            m[t][k] = nm[k];
+          }
+          const float f0 = nv2[0] == -INFINITY ? 1.0f : attn_exp2(mv[t][0] - nv2[0]);
+          const float f1 = nv2[1] == -INFINITY ? 1.0f : attn_exp2(mv[t][1] - nv2[1]);
+          mv[t][0] = nv2[0];
+          mv[t][1] = nv2[1];
+#pragma unroll
+          for (int i = 0; i < 2 * kNB; ++i) {
+            o[t][i][0] *= f0;
+            o[t][i][1] *= f1;
+            o[t][i][2] *= f0;
+            o[t][i][3] *= f1;
           }
         }
         const float m0 = m[t][0] == -INFINITY ? 0.0f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.0f : m[t][1];
-        x[0] = attn_exp2(x[0] - m0);
-        x[1] = attn_exp2(x[1] - m1);
-        x[2] = attn_exp2(x[2] - m0);
-        x[3] = attn_exp2(x[3] - m1);
-        l[t][0] += x[0] + x[2];
-        l[t][1] += x[1] + x[3];
-        // weights in bf16 (half a step 2^-9 of each, unbiased); the sum keeps fp32
-        pb[t][0] = attn_transpose8(attn_pack(x[0], x[1]));
-        pb[t][1] = attn_transpose8(attn_pack(x[2], x[3]));
+        const float v0 = mv[t][0] == -INFINITY ? 0.0f : mv[t][0], v1 = mv[t][1] == -INFINITY ? 0.0f : mv[t][1];
+        l[t][0] += attn_exp2(x[0] - m0) + attn_exp2(x[2] - m0);
+        l[t][1] += attn_exp2(x[1] - m1) + attn_exp2(x[3] - m1);
+        // weights in f16 (half a step 2^-11 of each); their sum l keeps fp32
+        pb[t][0] = attn_transpose8(attn_pack_f16(attn_exp2(x[0] + (e0 - v0)), attn_exp2(x[1] + (e0 - v1))));
+        pb[t][1] = attn_transpose8(attn_pack_f16(attn_exp2(x[2] + (e1 - v0)), attn_exp2(x[3] + (e1 - v1))));
       }
-      // ---- o^T += V^T P^T
-      const uint32_t fl = (attn_scale_pair<kFp8>(g.vs[0]) & 0xFFFFu) | (attn_scale_pair<kFp8>(g.vs[1]) << 16);
-      const uint32_t fh = (attn_scale_pair<kFp8>(g.vs[2]) & 0xFFFFu) | (attn_scale_pair<kFp8>(g.vs[3]) << 16);
-      bool slow = false;
-      if (kFp8) {
-        // a stored NaN: the rare way round, with NaN put in
-        uint32_t nv4 = 0u;
+      // ---- o^T += V^T P^T, a block at a time: lane r has channels 4 r .. 4 r + 3 of the block
+      attn_copy_wait<2 * kS - 1>();
+      __syncwarp();
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+      for (int b = 0; b < kNB; ++b) {
+        if (b >= p.nb) break;
+        const uint2 f = *reinterpret_cast<const uint2*>(fv + b * 16 + 4 * c);
+        uint32_t v[4][2];  // channel 4 r + k: tokens (2c, 2c + 1), (2c + 8, 2c + 9)
+        const uint8_t* src = vt + 2 * c * C::kVs;
+        if (kFp8) {
 #pragma unroll
-          for (int k = 0; k < kVw; ++k) nv4 |= attn_e4m3_nan(g.v[x][k]);
-        slow = __any_sync(0xffffffffu, (nv4 & 0x80808080u) != 0u);
-      }
-#pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        uint32_t a[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int d = 2 * i + e;  // the lane's channel
-          uint32_t lo, hi;
-          if (kFp8) {
-            const int by = d & 3;
-            const uint32_t sel = static_cast<uint32_t>(by) << 4 | static_cast<uint32_t>(4 + by) << 12;
-            lo = attn_e4m3_bits(__byte_perm(g.v[0][d >> 2], g.v[1][d >> 2], sel));
-            hi = attn_e4m3_bits(__byte_perm(g.v[2][d >> 2], g.v[3][d >> 2], sel));
-            if (slow) {
-              lo = attn_nan_pair(lo);
-              hi = attn_nan_pair(hi);
-            }
-          } else {
-            const int by = (d & 7) >> 1;
-            const uint32_t sel = static_cast<uint32_t>(by) << 4 | static_cast<uint32_t>(4 + by) << 12;
-            uint32_t x0 = __byte_perm(g.v[0][d >> 3], g.v[1][d >> 3], sel);
-            uint32_t x1 = __byte_perm(g.v[2][d >> 3], g.v[3][d >> 3], sel);
-            if (!(d & 1)) {
-              x0 <<= 4;
-              x1 <<= 4;
-            }
-            lo = attn_e2m1_bits(x0);
-            hi = attn_e2m1_bits(x1);
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(src + 8 * x * C::kVs + 32 * b + 4 * r);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(src + (8 * x + 1) * C::kVs + 32 * b + 4 * r);
+            attn_e4m3_f16(__byte_perm(w0, w1, 0x5140), v[0][x], v[1][x]);
+            attn_e4m3_f16(__byte_perm(w0, w1, 0x7362), v[2][x], v[3][x]);
           }
-          a[e] = attn_mul_bf16x2(lo, fl);
-          a[2 + e] = attn_mul_bf16x2(hi, fh);
+        } else {
+          // nibbles of the same channel side by side: even channels, odd channels
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = *reinterpret_cast<const uint16_t*>(src + ((x & 1) + 8 * (x >> 1)) * C::kVs + 16 * b + 2 * r);
+          const uint32_t a = w[0] | w[2] << 16, d = w[1] | w[3] << 16;
+          uint32_t ev[4], od[4];
+          attn_e2m1_f16((a & 0x0F0F0F0Fu) | ((d << 4) & 0xF0F0F0F0u), ev);
+          attn_e2m1_f16(((a >> 4) & 0x0F0F0F0Fu) | (d & 0xF0F0F0F0u), od);
+          v[0][0] = ev[0];
+          v[2][0] = ev[1];
+          v[0][1] = ev[2];
+          v[2][1] = ev[3];
+          v[1][0] = od[0];
+          v[3][0] = od[1];
+          v[1][1] = od[2];
+          v[3][1] = od[3];
         }
 #pragma unroll
-        for (int t = 0; t < kNT; ++t) attn_mma(o[t][i], a[0], a[1], a[2], a[3], pb[t][0], pb[t][1]);
+        for (int t = 0; t < kNT; ++t) {
+          const uint32_t q0 = attn_mul_f16x2(pb[t][0], f.x), q1 = attn_mul_f16x2(pb[t][1], f.y);
+          attn_mma_f16(o[t][2 * b], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
+          attn_mma_f16(o[t][2 * b + 1], v[2][0], v[3][0], v[2][1], v[3][1], q0, q1);
+        }
       }
-      load_v(rows_next);
-      rows_now = rows_next;
-      rows_next = rows_after;
+      __syncwarp();
+      copy_v(rw[kS], st);
+      if (++st == kS) st = 0;
+#pragma unroll
+      for (int k = 0; k < kS; ++k) rw[k] = rw[k + 1];
     }
+    attn_copy_wait<0>();
+    __syncthreads();  // the rings are free
 
     // ---- join the warps
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
+      float f[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+      for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
-      if (r == 0) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        f[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(mv[t][k] - m[t][k]);
+        if (r == 0) {
           float* ml = sml + (warp * kR + 8 * t + 2 * c + k) * 2;
           ml[0] = m[t][k];
           ml[1] = l[t][k];
         }
       }
 #pragma unroll
-      for (int i = 0; i < kMT; ++i) {
-        // rows r and r + 8 of the tile are the lane's channels 16 kNB4 r + 2 i and + 1
-        const int d = 16 * kNB4 * r + 2 * i;
+      for (int i = 0; i < 2 * kNB; ++i) {
+        // rows r and r + 8 of m-tile i are channels 32 (i / 2) + 4 r + 2 (i % 2) and the next
+        const int d = 32 * (i >> 1) + 4 * r + 2 * (i & 1);
         float* o0 = so + (warp * kR + 8 * t + 2 * c) * kLdo + d;
-        *reinterpret_cast<float2*>(o0) = make_float2(o[t][i][0], o[t][i][2]);
-        *reinterpret_cast<float2*>(o0 + kLdo) = make_float2(o[t][i][1], o[t][i][3]);
+        *reinterpret_cast<float2*>(o0) = make_float2(o[t][i][0] * f[0], o[t][i][2] * f[0]);
+        *reinterpret_cast<float2*>(o0 + kLdo) = make_float2(o[t][i][1] * f[1], o[t][i][3] * f[1]);
       }
     }
     __syncthreads();
     const bool whole = first == 0 && last == pl.chunks;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (seg == 0 ? 0 : 1);
-    float* dst = whole ? so : p.part_o + static_cast<int64_t>(slot) * kR * p.D;
+    float* dst = whole ? sy : p.part_o + static_cast<int64_t>(slot) * kR * p.D;
     const int ldd = whole ? kLdo : p.D;
     float* dml = whole ? fml : p.part_ml + static_cast<int64_t>(slot) * kR * 2;
-    for (int i = threadIdx.x; i < nrows * p.D; i += attn::kThreads) {
-      const int n = i / p.D, d = i - n * p.D;
-      float mm = -INFINITY;
-      bool bad = false;
+    const int quads = p.D >> 2;
+    for (int i = threadIdx.x; i < nrows * quads; i += attn::kThreads) {
+      const int n = i / quads, d = 4 * (i - n * quads);
+      float mm = -INFINITY, f[attn::kWarps], sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < attn::kWarps; ++w) mm = fmaxf(mm, sml[(w * kR + n) * 2]);
 #pragma unroll
       for (int w = 0; w < attn::kWarps; ++w) {
-        const float mw = sml[(w * kR + n) * 2];
-        mm = fmaxf(mm, mw);
-        bad |= sml[(w * kR + n) * 2 + 1] != sml[(w * kR + n) * 2 + 1];
+        const float2 ml = *reinterpret_cast<const float2*>(sml + (w * kR + n) * 2);
+        f[w] = ml.x == -INFINITY ? 0.0f : attn_exp2(ml.x - mm);
+        sum = ml.y != ml.y ? NAN : __fmaf_rn(ml.y, f[w], sum);  // (a NaN stays: NaN * f + anything)
       }
-      float acc = 0.0f, sum = 0.0f;
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < attn::kWarps; ++w) {
-        const float mw = sml[(w * kR + n) * 2];
-        const float f = mw == -INFINITY ? 0.0f : attn_exp2(mw - mm);
-        acc = __fmaf_rn(so[(w * kR + n) * kLdo + d], f, acc);
-        sum = __fmaf_rn(sml[(w * kR + n) * 2 + 1], f, sum);
+        const float4 v = *reinterpret_cast<const float4*>(so + (w * kR + n) * kLdo + d);
+        acc.x = __fmaf_rn(v.x, f[w], acc.x);
+        acc.y = __fmaf_rn(v.y, f[w], acc.y);
+        acc.z = __fmaf_rn(v.z, f[w], acc.z);
+        acc.w = __fmaf_rn(v.w, f[w], acc.w);
       }
-      if (bad) acc = sum = NAN;
-      // warp 0's slice is read by this thread alone at (n, d): the sum may replace it
-      dst[n * ldd + d] = acc;
-      if (d == 0) {
+      if (whole) {
+        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (p.oa == nullptr)
+          *reinterpret_cast<uint2*>(p.out + (tok * p.Hq + head0 + n) * p.D + d) =
+              make_uint2(attn_pack(acc.x, acc.y), attn_pack(acc.z, acc.w));
+        if (p.lse && d == 0)
+          p.lse[tok * p.Hq + head0 + n] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * 0.69314718055994531f;
+      } else if (d == 0) {
         dml[2 * n] = mm;
         dml[2 * n + 1] = sum;
       }
+      if (!whole || p.oa != nullptr) *reinterpret_cast<float4*>(dst + n * ldd + d) = acc;
+    }
+    if (whole && p.oa != nullptr) {
+      __syncthreads();
+      for (int i = threadIdx.x; i < nrows * p.nb * 8; i += attn::kThreads) {
+        const int q = i & 7, blk = (i >> 3) % p.nb, n = (i >> 3) / p.nb;
+        float y[4];
+        attn_block_apply(fo, blk, sy + n * kLdo + 32 * blk, q, y);
+        uint16_t* out = p.out + (tok * p.Hq + head0 + n) * p.D + 32 * blk + q;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[8 * j] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
+      }
     }
     __syncthreads();
-    if (whole) {
-      attn_finish(p, so, kLdo, fml, nrows, p.oa ? po : nullptr, [&](int n, int64_t& t, int& hd) {
-        t = tok;
-        hd = head0 + n;
-        return true;
-      });
-      __syncthreads();
-    }
     left -= last - first;
     if (left > 0) attn_next_unit<0>(p, pl, seq);
   }
@@ -836,20 +891,19 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i1 = blockIdx.x + 1;
   float* so = smem + warp * 260;  // [D] of this warp's row, its maximum and sum
-  float* po = nullptr;
+  AttnFactors fo{nullptr, nullptr, 3};
+  if (p.oa) fo = attn_stage_factors(smem + 8 * 260, p.oa, p.ob, p.nb, p.ols);
+  __syncthreads();
   grid_dependency_wait();
   const AttnMark mk = p.marks[i1];
   const int64_t total = mk.total, x = mk.x;
   if (x >= total) return;
   const AttnPlace pl = mk.place;
+  const AttnDeal deal(total, p.ctas);
   const int64_t u0 = x - pl.chunk, u1 = u0 + pl.chunks;
-  if (pl.chunk == 0 || attn_start(total, i1 - 1, p.ctas) > u0) return;  // no split here, or an earlier CTA's
+  if (pl.chunk == 0 || deal.start(i1 - 1) > u0) return;  // no split here, or an earlier CTA's
   int end = i1 + 1;  // parts of CTAs [i1 - 1, end)
-  while (end < p.ctas && attn_start(total, end, p.ctas) < u1) ++end;
-  if (p.oa) {
-    po = smem + 8 * 260 + kv::kFacFloats;
-    kv_build_p(po, smem + 8 * 260, p.oa, p.ob, p.nb, p.ols);
-  }
+  while (end < p.ctas && deal.start(end) < u1) ++end;
   const int rows = p.unit_rows;
   const AttnSeq seq = attn_seq(p, pl.b);
   const int hgs = p.head_units / p.Hkv;
@@ -875,8 +929,8 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
     for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.0f, 0.0f);
     bool bad = false;
     for (int i = i1 - 1; i < end; ++i) {
-      const int64_t xi = attn_start(total, i, p.ctas);
-      if (xi >= attn_start(total, i + 1, p.ctas)) continue;  // an empty run
+      const int64_t xi = deal.start(i);
+      if (xi >= deal.start(i + 1)) continue;  // an empty run
       // the unit is the first of CTA i's run if the run begins inside the unit (or at it)
       const int64_t at = (2 * static_cast<int64_t>(i) + (xi >= u0 ? 0 : 1)) * rows + rr;
       const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
@@ -898,33 +952,30 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
         }
     }
     if (bad) sum = NAN;
-    const float inv = sum > 0.0f ? attn::kUp / sum : (sum == 0.0f ? 0.0f : sum);
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
     uint16_t* dst = p.out + (tok * p.Hq + head) * p.D;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
+      const int d = 64 * k + 2 * lane;
       acc[k].x *= inv;
       acc[k].y *= inv;
-      if (po != nullptr && 64 * k + 2 * lane < p.D) *reinterpret_cast<float2*>(so + 64 * k + 2 * lane) = acc[k];
-    }
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int d = 64 * k + 2 * lane;
       if (d >= p.D) break;
-      if (po != nullptr) {
-        const float* src = so + (d & ~31);
-        const float* pb = po + (d >> 5) * 1024 + (d & 31);
-        acc[k] = make_float2(0.0f, 0.0f);
-#pragma unroll 8
-        for (int j = 0; j < 32; ++j) {
-          const float2 cf = *reinterpret_cast<const float2*>(pb + 32 * j);
-          acc[k].x = __fmaf_rn(src[j], cf.x, acc[k].x);
-          acc[k].y = __fmaf_rn(src[j], cf.y, acc[k].y);
-        }
-      }
-      *reinterpret_cast<uint32_t*>(dst + d) = attn_pack(acc[k].x, acc[k].y);
+      if (p.oa != nullptr)
+        *reinterpret_cast<float2*>(so + d) = acc[k];
+      else
+        *reinterpret_cast<uint32_t*>(dst + d) = attn_pack(acc[k].x, acc[k].y);
     }
-    __syncwarp();
+    if (p.oa != nullptr) {
+      __syncwarp();
+      for (int i = lane; i < p.nb * 8; i += 32) {
+        float y[4];
+        attn_block_apply(fo, i >> 3, so + 32 * (i >> 3), i & 7, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          dst[32 * (i >> 3) + 8 * j + (i & 7)] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
+      }
+      __syncwarp();
+    }
     if (p.lse && lane == 0)
       p.lse[tok * p.Hq + head] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * 0.69314718055994531f;
   }

@@ -243,14 +243,12 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     tmem_relinquish();
   }
   if (warp == 15) {
-    const int64_t total = attn_total<kTile>(p, lane);
-    const int64_t x0 = attn_start(total, blockIdx.x, p.ctas), x1 = attn_start(total, blockIdx.x + 1, p.ctas);
-    AttnPlace pl{};
-    if (x0 < total) pl = attn_locate<kTile>(p, x0, lane);
+    int64_t n;
+    const AttnMark mk = attn_mark<kTile>(p, blockIdx.x, lane, n);
     if (lane == 0) {
-      s_place = pl;
-      s_run = x1 - x0;
-      p.marks[blockIdx.x] = AttnMark{x0, total, pl};
+      s_place = mk.place;
+      s_run = n;
+      p.marks[blockIdx.x] = mk;
     }
   }
   if (p.oa != nullptr && p.ols == 3 && warp == 14) {
@@ -491,7 +489,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
         tmem_ld_32x32b_x32(o_col(t) + lane_base + 32 * b, o);
         tmem_wait_ld();
         float v[32];
-        const float f = part ? 1.0f : inv;
+        const float f = part ? attn::kUp : inv;
         // (a row that saw nothing: its sums are 0, whatever a NaN in q may have left in them)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[attn_v_order<kFp8>(j)] = l == 0.0f ? 0.0f : __uint_as_float(o[j]) * f;
