@@ -656,7 +656,7 @@ bat_status_t check_gemm_args(const bat_mxfp4_t* Xq, const bat_mxfp4_t* Wq, const
 namespace {
 
 // CTAs that the chunks are dealt over: the workspace holds two partial results for each.
-constexpr int kAttnRowCtas = 296;
+constexpr int kAttnRowCtas = 592;
 
 // Row kernel: heads of a KV head that one unit takes.
 int attn_row_unit(int64_t G, int64_t D) { return G > 8 && D <= 128 ? 16 : 8; }
@@ -720,9 +720,10 @@ bat_status_t launch_attn_rows(bat::AttnParams& p, int dev, int sms, int bit, cud
                                                      (p.oa ? bat::attn_factor_floats(p.nb, p.ols) : 0));
   bat_status_t st = attn_smem(k, dev, bit, attn_rows_smem<kFp8, kNB, kNT>(2 * bat::kv::kFacFloats));
   if (st != BAT_OK) return st;
-  // two CTAs an SM where registers and shared memory allow; a few chunks need fewer CTAs,
-  // but how many there are is known on the device only
-  const int per_sm = kNB * kNT <= 4 && smem <= 112 * 1024 ? 2 : 1;
+  // every CTA that can be resident (few chunks need fewer, but how many there are is known on
+  // the device only)
+  int per_sm = bat::attn_rows_per_sm(kFp8, kNB, kNT);
+  while (per_sm > 1 && per_sm * (smem + 2048) > 227 * 1024) --per_sm;
   p.ctas = per_sm * sms < kAttnRowCtas ? per_sm * sms : kAttnRowCtas;
   k<<<p.ctas, bat::attn::kThreads, smem, s>>>(p);
   return cuda_status(cudaGetLastError());
@@ -1173,16 +1174,17 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
   p.T = T;
-  p.num_slots = K->num_slots;
   p.capacity = max_pages > kMaxRows / page_size ? kMaxRows : max_pages * page_size;
   p.B = static_cast<int>(B);
   p.max_pages = static_cast<int>(max_pages);
   p.page_size = static_cast<int>(page_size);
-  // division by a constant for 31-bit numerators: l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1
+  // division by a constant for 31-bit numerators: l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1 < 2^32
   int pl = 0;
   while ((int64_t{1} << pl) < page_size) ++pl;
-  p.page_shift = 31 + pl;
-  p.page_mul = static_cast<uint32_t>((uint64_t{1} << (31 + pl)) / static_cast<uint64_t>(page_size) + 1);
+  p.page_shift = pl - 1;
+  p.page_mul = page_size == 1 ? 0u : static_cast<uint32_t>((uint64_t{1} << (31 + pl)) / static_cast<uint64_t>(page_size) + 1);
+  p.pages = static_cast<uint32_t>((K->num_slots + page_size - 1) / page_size);
+  p.slots = static_cast<uint32_t>(K->num_slots);
   p.Hq = static_cast<int>(Hq);
   p.Hkv = static_cast<int>(H);
   p.G = static_cast<int>(Hq / H);

@@ -29,7 +29,7 @@ namespace bat {
 
 namespace attn {
 constexpr int kChunk = 128;   // visible tokens a chunk
-constexpr int kWarps = 8;     // row kernel: warps a CTA, 16 tokens of a chunk each
+constexpr int kWarps = 4;     // row kernel: warps a CTA, 32 tokens of a chunk each
 constexpr int kThreads = 32 * kWarps;
 // V's stored elements go to bf16 through their bits, which leaves them 2^120 (E4M3) or 2^126
 // (E2M1) too small; the MX scale's multiplication puts that right up to 2^-32, so that
@@ -68,11 +68,12 @@ struct AttnParams {
   float* part_o;           // [2 * ctas][rows][D], unnormalised
   float* part_ml;          // [2 * ctas][rows][2]
   AttnMark* marks;         // [ctas]
-  int64_t T, num_slots;
+  int64_t T;
   int64_t capacity;        // max_pages * page_size
   int B, max_pages, page_size;
-  uint32_t page_mul;       // j / page_size = (j * page_mul) >> page_shift for 0 <= j < 2^31
+  uint32_t page_mul;       // j / page_size = (j * page_mul) >> (32 + page_shift) for 0 <= j < 2^31
   int page_shift;
+  uint32_t pages, slots;   // of the cache: ceil(slots / page_size), slots (< 2^30)
   int Hq, Hkv, G, D, nb;
   int qls, ols;
   int window, sinks;       // window 0: none
@@ -246,18 +247,21 @@ __device__ __forceinline__ void attn_next_unit(const AttnParams& p, AttnPlace& p
 // Cache row (slot * Hkv + head) of token j of a sequence, or -1 for a page outside the cache, in
 // two steps, so that the table's entry can be on its way while other work is done.
 __device__ __forceinline__ int attn_page_of(const AttnParams& p, int j) {
-  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(j)) * p.page_mul) >> p.page_shift);
+  // (page_mul 0: pages of one token)
+  return p.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(j), p.page_mul) >> p.page_shift) : j;
 }
-__device__ __forceinline__ int attn_row_at(const AttnParams& p, int page, int j, int h) {
-  const int64_t slot = static_cast<int64_t>(page) * p.page_size + (j - attn_page_of(p, j) * p.page_size);
-  if (slot < 0 || slot >= p.num_slots) {
+__device__ __forceinline__ int attn_row_at(const AttnParams& p, int page, int offset, int h) {
+  // pages within the cache: their slots fit 30 bits
+  const uint32_t slot = static_cast<uint32_t>(page) * static_cast<uint32_t>(p.page_size) + static_cast<uint32_t>(offset);
+  if (static_cast<uint32_t>(page) >= p.pages || slot >= p.slots) {
     atomicOr(&g_dev_error, kErrBadIndex);
     return -1;
   }
-  return static_cast<int>(slot * p.Hkv + h);
+  return static_cast<int>(slot * static_cast<uint32_t>(p.Hkv) + static_cast<uint32_t>(h));
 }
 __device__ __forceinline__ int attn_cache_row(const AttnParams& p, const int32_t* pages, int j, int h) {
-  return attn_row_at(p, __ldg(pages + attn_page_of(p, j)), j, h);
+  const int pg = attn_page_of(p, j);
+  return attn_row_at(p, __ldg(pages + pg), j - pg * p.page_size, h);
 }
 
 __device__ __forceinline__ float attn_exp2(float x) {
@@ -406,38 +410,43 @@ __device__ __forceinline__ void attn_block_apply(const AttnFactors& f, int blk, 
 }
 
 // ---------------------------------------------------------------- few rows (decode)
-// A unit is one token and up to 8 kNT of its heads that share a KV head; a warp takes 16 of
-// the chunk's 128 tokens, keeps its own running maximum, sum and o, and the eight warps join
+// A unit is one token and up to 8 kNT of its heads that share a KV head; a warp takes 32 of
+// the chunk's 128 tokens, keeps its own running maximum, sum and o, and the four warps join
 // at the unit's end. Products on mma.sync with the tokens on the 16-row side,
 //   S^T = K q^T (16 tokens x 8 heads),   o^T += V^T P^T (channels x 16 tokens),
 // so that 8 heads fill the other side. All rows of a unit see the same tokens, so a masked token is
 // simply not loaded (zeros in its place).
 // Each warp streams its tokens through its own ring in shared memory (16-byte asynchronous
-// copies, kStages tiles of K and of V in flight, refilled as soon as a tile is used), so no
+// copies, kStages tiles of 32 tokens, refilled as soon as a tile is used), so no
 // barrier is met between a unit's start and its end, and the loads' latency is covered whatever
-// the lengths (loads to registers one tile ahead: 2.0-2.5 us a chunk where this takes 1.0-1.4).
+// the lengths. A lane looks up one token of the tile, its page, row and scales.
 // Scales: S^T of each 32-channel block is multiplied by the tokens' K scales in fp32. For V, with E
 // the largest scale exponent of a token, the weights are taken as
 //   w = 2^(x + E - M),  M the running maximum of x + E  (x: the score in log2 units),
 // and multiplied by 2^(e_b - E) <= 1 for block b, so V's codes enter the product as they are.
-// Bound: HBM bytes for KV8; about 300 instructions a warp and tile, near the issue limit, for KV4.
+// Bound: HBM bytes for KV8, about equally the issue slots for KV4.
 template <bool kFp8, int kNB>
 struct AttnRowCfg {
+  static constexpr int kTok = 32;                            // tokens of a warp's tile
   static constexpr int kBytes = kFp8 ? 32 * kNB : 16 * kNB;  // codes of a token, padded to kNB blocks
   // row strides in shared memory that keep the fragment loads free of bank conflicts: K is read
   // by 8 bytes (E4M3) at 8 c of tokens r, by 4 (E2M1); V by 4 or 2 bytes of tokens 2c
   static constexpr int kKs = kFp8 ? kBytes + 32 : kBytes + 16;
   static constexpr int kVs = kBytes + 16;
-  static constexpr int kStages = kFp8 ? (kNB == 2 ? 3 : 2) : (kNB == 2 ? 4 : (kNB == 4 ? 3 : 2));
-  static constexpr int kStageBytes = 16 * (kKs + kVs);
-  // factors of a tile: K scales fp32 [16][kNB], V factors f16 [kNB][16], E fp32 [16]
-  static constexpr int kFacBytes = 16 * kNB * 4 + 16 * kNB * 2 + 64;
+  static constexpr int kStages = !kFp8 && kNB == 2 ? 3 : 2;
+  static constexpr int kStageBytes = kTok * (kKs + kVs);
+  // factors of a tile: K scales fp32 [32][kNB], V factors f16 [kNB][32], E fp32 [32]
+  static constexpr int kFacBytes = kTok * kNB * 4 + kTok * kNB * 2 + kTok * 4;
   static constexpr int kWarpBytes = kStages * kStageBytes + 2 * kFacBytes;
 };
 constexpr size_t attn_rows_ring_bytes(int warp_bytes, int nt, int nb) {
   const size_t ring = static_cast<size_t>(attn::kWarps) * warp_bytes;
   const size_t join = static_cast<size_t>(attn::kWarps) * 8 * nt * (32 * nb + 4) * 4;  // takes the ring's place
   return ring > join ? ring : join;
+}
+// CTAs an SM that registers and shared memory allow.
+constexpr int attn_rows_per_sm(bool fp8, int nb, int nt) {
+  return nb * nt <= 4 ? (fp8 && nb == 4 ? 2 : 4) : (fp8 && nb == 8 ? 1 : 2);
 }
 
 __device__ __forceinline__ void attn_copy16(uint32_t dst, const void* src, bool ok) {
@@ -450,7 +459,7 @@ __device__ __forceinline__ void attn_copy_wait() {
 }
 
 template <bool kFp8, int kNB, int kNT>
-__global__ void __launch_bounds__(attn::kThreads, kNB * kNT <= 4 ? 2 : 1) bat_attn_rows_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kNT)) bat_attn_rows_kernel(const AttnParams p) {
   using C = AttnRowCfg<kFp8, kNB>;
   extern __shared__ __align__(16) float smem[];
   constexpr int kDP = 32 * kNB, kR = 8 * kNT, kS = C::kStages;
@@ -503,71 +512,111 @@ __global__ void __launch_bounds__(attn::kThreads, kNB * kNT <= 4 ? 2 : 1) bat_at
     const int last = static_cast<int>(min(static_cast<int64_t>(pl.chunks), first + left));  // chunks [first, last)
     const int32_t* pages = p.table + static_cast<int64_t>(pl.b) * p.max_pages;
 
-    // ---- the warp's stream: token `lane & 15` of its tiles
-    int j_ahead, page_ahead = 0;
+    // ---- the warp's stream: a lane a token of its tiles
+    int page_ahead = 0, off_ahead = -1;
     auto look = [&](int chunk) {
-      const int i = chunk * attn::kChunk + 16 * warp + (lane & 15);
-      j_ahead = chunk < last && i < nv ? span.token(i) : -1;
-      if (j_ahead >= 0) page_ahead = __ldg(pages + attn_page_of(p, j_ahead));
+      const int i = chunk * attn::kChunk + 32 * warp + lane;
+      off_ahead = -1;
+      if (chunk >= last || i >= nv) return;
+      const int j = span.token(i), pg = attn_page_of(p, j);
+      page_ahead = __ldg(pages + pg);
+      off_ahead = j - pg * p.page_size;
     };
-    auto found = [&]() -> int { return j_ahead >= 0 ? attn_row_at(p, page_ahead, j_ahead, h) : -1; };
-    constexpr int kPieces = C::kBytes / 16;
-    auto copy = [&](int rows16, const uint8_t* codes, uint32_t dst, int stride) {
+    auto found = [&]() -> int { return off_ahead >= 0 ? attn_row_at(p, page_ahead, off_ahead, h) : -1; };
+    // two lanes copy 32 bytes of a token each time
+    auto copy = [&](int row, int st) {
+      const uint32_t kd = ring32 + st * C::kStageBytes + (lane >> 1) * C::kKs + (lane & 1) * 16;
+      const uint32_t vd = ring32 + st * C::kStageBytes + C::kTok * C::kKs + (lane >> 1) * C::kVs + (lane & 1) * 16;
 #pragma unroll
-      for (int k = 0; k < 16 * kPieces / 32; ++k) {
-        const int tk = (32 * k + lane) / kPieces, piece = (32 * k + lane) % kPieces;
-        const int row = __shfl_sync(0xffffffffu, rows16, tk);
-        const bool ok = row >= 0 && 16 * piece < row_bytes;
-        attn_copy16(dst + tk * stride + 16 * piece, ok ? codes + static_cast<int64_t>(row) * row_bytes + 16 * piece : codes, ok);
+      for (int x = 0; x < 2; ++x) {
+        const int rx = __shfl_sync(0xffffffffu, row, (lane >> 1) + 16 * x);
+        const int64_t off = static_cast<int64_t>(max(rx, 0)) * row_bytes + (lane & 1) * 16;
+        const uint8_t* ks = p.k_codes + off;
+        const uint8_t* vs = p.v_codes + off;
+#pragma unroll
+        for (int k = 0; k < C::kBytes; k += 32) {
+          // (a row of 16 bytes, one block of E2M1, has no second half)
+          const bool in = kFp8 ? k < row_bytes : k + (lane & 1) * 16 < row_bytes;
+          if (k > 0 && !(k < row_bytes)) break;
+          attn_copy16(kd + 16 * x * C::kKs + k, in ? ks + k : p.k_codes, in && rx >= 0);
+          attn_copy16(vd + 16 * x * C::kVs + k, in ? vs + k : p.v_codes, in && rx >= 0);
+        }
       }
       attn_copy_commit();
     };
-    auto copy_k = [&](int rows16, int st) { copy(rows16, p.k_codes, ring32 + st * C::kStageBytes, C::kKs); };
-    auto copy_v = [&](int rows16, int st) { copy(rows16, p.v_codes, ring32 + st * C::kStageBytes + 16 * C::kKs, C::kVs); };
-    // scale bytes of the lane's token: K's for lanes 0..15, V's for 16..31, four a word
-    uint32_t sc[(kNB + 3) / 4];
+    // the lane's token's scale bytes, four a word
+    constexpr int kW = (kNB + 3) / 4;
+    uint32_t sck[kW], scv[kW];
     auto load_scales = [&](int row) {
-      const uint8_t* src = (lane < 16 ? p.k_scales : p.v_scales) + static_cast<int64_t>(row) * p.nb;
+      const int64_t at = static_cast<int64_t>(max(row, 0)) * p.nb;
 #pragma unroll
-      for (int w = 0; w < (kNB + 3) / 4; ++w) {
-        sc[w] = 0u;
+      for (int w = 0; w < kW; ++w) {
+        sck[w] = scv[w] = 0u;
         if (row < 0) continue;
         if (p.scale_words) {
-          sc[w] = 4 * w < p.nb ? __ldg(reinterpret_cast<const uint32_t*>(src) + w) : 0u;
+          if (4 * w < p.nb) {
+            sck[w] = __ldg(reinterpret_cast<const uint32_t*>(p.k_scales + at) + w);
+            scv[w] = __ldg(reinterpret_cast<const uint32_t*>(p.v_scales + at) + w);
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (4 * w + k < p.nb) sc[w] |= static_cast<uint32_t>(__ldg(src + 4 * w + k)) << (8 * k);
+            if (4 * w + k < p.nb) {
+              sck[w] |= static_cast<uint32_t>(__ldg(p.k_scales + at + 4 * w + k)) << (8 * k);
+              scv[w] |= static_cast<uint32_t>(__ldg(p.v_scales + at + 4 * w + k)) << (8 * k);
+            }
         }
       }
     };
     auto put_scales = [&](int par) {
       float* fk = reinterpret_cast<float*>(facs + par * C::kFacBytes);
-      uint16_t* fv = reinterpret_cast<uint16_t*>(fk + 16 * kNB);
-      float* fe = reinterpret_cast<float*>(fv + 16 * kNB);
-      const int tk = lane & 15;
-      if (lane < 16) {
+      uint16_t* fv = reinterpret_cast<uint16_t*>(fk + C::kTok * kNB);
+      float* fe = reinterpret_cast<float*>(fv + C::kTok * kNB);
+      uint32_t nan = 0u;  // a byte 255
 #pragma unroll
-        for (int b = 0; b < kNB; ++b) fk[tk * kNB + b] = attn_scale_value((sc[b / 4] >> (8 * (b & 3))) & 255u);
-      } else {
-        int top = 0;
+      for (int w = 0; w < kW; ++w)
+        nan |= (((sck[w] & 0x7F7F7F7Fu) + 0x01010101u) & sck[w]) | (((scv[w] & 0x7F7F7F7Fu) + 0x01010101u) & scv[w]);
+      nan &= 0x80808080u;
+      float kf[kNB];
+      int top = 0;
 #pragma unroll
-        for (int b = 0; b < kNB; ++b) {
-          const int e = (sc[b / 4] >> (8 * (b & 3))) & 255u;
-          top = e != 255 ? max(top, e) : top;
-        }
-        // tokens 2c, 2c + 1, 2c + 8, 2c + 9 side by side
-        const int at = (tk & 6) * 2 + (tk & 1) + (tk >> 3) * 2;
-#pragma unroll
-        for (int b = 0; b < kNB; ++b) {
-          const int e = (sc[b / 4] >> (8 * (b & 3))) & 255u;
-          fv[b * 16 + at] = static_cast<uint16_t>(e == 255 ? 0x7E00u : attn_f16_pow2(top - e));
-        }
-        fe[tk] = static_cast<float>(top - 127);
+      for (int b = 0; b < kNB; ++b) {
+        const int ek = (sck[b / 4] >> (8 * (b & 3))) & 255u, ev = (scv[b / 4] >> (8 * (b & 3))) & 255u;
+        kf[b] = __uint_as_float(max(static_cast<uint32_t>(ek) << 23, 0x00400000u));  // (byte 0: 2^-127)
+        top = max(top, ev);
       }
+      if (nan) {
+        top = 0;
+        for (int b = 0; b < kNB; ++b) {
+          const int ev = (scv[b / 4] >> (8 * (b & 3))) & 255u;
+          top = ev != 255 ? max(top, ev) : top;
+        }
+      }
+      // tokens 2c, 2c + 1, 2c + 8, 2c + 9 of a half side by side
+      const int at = (lane & 16) + (lane & 6) * 2 + (lane & 1) + ((lane >> 3) & 1) * 2;
+#pragma unroll
+      for (int b = 0; b < kNB; b += 2) {
+        // 2^(e - top), by fp32 to f16 (which takes care of what is below its normal range)
+        const int e0 = (scv[b / 4] >> (8 * (b & 3))) & 255u, e1 = (scv[b / 4] >> (8 * (b & 3) + 8)) & 255u;
+        const float f0 = __uint_as_float(static_cast<uint32_t>(max(127 + e0 - top, 0)) << 23);
+        const float f1 = __uint_as_float(static_cast<uint32_t>(max(127 + e1 - top, 0)) << 23);
+        uint32_t f = attn_pack_f16(f0, f1);
+        if (nan) {
+          if (e0 == 255) f |= 0x7FFFu;
+          if (e1 == 255) f |= 0x7FFF0000u;
+          if (((sck[b / 4] >> (8 * (b & 3))) & 255u) == 255u) kf[b] = NAN;
+          if (((sck[b / 4] >> (8 * (b & 3) + 8)) & 255u) == 255u) kf[b + 1] = NAN;
+        }
+        fv[b * 32 + at] = static_cast<uint16_t>(f);
+        fv[(b + 1) * 32 + at] = static_cast<uint16_t>(f >> 16);
+      }
+#pragma unroll
+      for (int b = 0; b < kNB; b += 2)
+        *reinterpret_cast<float2*>(fk + lane * kNB + b) = make_float2(kf[b], kf[b + 1]);
+      fe[lane] = static_cast<float>(top - 127);
     };
 
-    int rw[kS + 1];  // cache rows of tiles i .. i + kS - 1 of the warp
+    int rw[kS + 1];  // cache rows of tiles i .. i + kS - 1 of the warp, a token a lane
 #pragma unroll
     for (int k = 0; k < kS; ++k) {
       look(first + k);
@@ -575,10 +624,7 @@ __global__ void __launch_bounds__(attn::kThreads, kNB * kNT <= 4 ? 2 : 1) bat_at
     }
     load_scales(rw[0]);
 #pragma unroll
-    for (int k = 0; k < kS; ++k) {
-      copy_k(rw[k], k);
-      copy_v(rw[k], k);
-    }
+    for (int k = 0; k < kS; ++k) copy(rw[k], k);
     look(first + kS);
 
     // ---- q rows (times P_q) in fp32, then in f16 with the row's power of two
@@ -658,140 +704,159 @@ __global__ void __launch_bounds__(attn::kThreads, kNB * kNT <= 4 ? 2 : 1) bat_at
       look(ch + kS + 1);
       put_scales(par ^ 1);
       load_scales(rw[2]);
-      attn_copy_wait<2 * kS - 1>();
+      attn_copy_wait<kS - 1>();
       __syncwarp();
       const uint8_t* kt = ring + st * C::kStageBytes;
-      const uint8_t* vt = kt + 16 * C::kKs;
+      const uint8_t* vt = kt + C::kTok * C::kKs;
       const float* fk = reinterpret_cast<const float*>(facs + par * C::kFacBytes);
-      const uint16_t* fv = reinterpret_cast<const uint16_t*>(fk + 16 * kNB);
-      const float* fe = reinterpret_cast<const float*>(fv + 16 * kNB);
-      // ---- S^T = K q^T, a block at a time
-      float s[kNT][4];
+      const uint16_t* fv = reinterpret_cast<const uint16_t*>(fk + C::kTok * kNB);
+      const float* fe = reinterpret_cast<const float*>(fv + C::kTok * kNB);
+      // ---- S^T = K q^T for the tile's halves of 16 tokens, a block at a time
+      float s[2][kNT][4];
 #pragma unroll
-      for (int t = 0; t < kNT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < kNT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.0f;
 #pragma unroll
       for (int b = 0; b < kNB; ++b) {
         if (b >= p.nb) break;
-        uint32_t a[2][4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint8_t* src = kt + (r + 8 * x) * C::kKs;
-          if (kFp8) {
-            const uint2 w = *reinterpret_cast<const uint2*>(src + 32 * b + 8 * c);
-            attn_e4m3_f16(w.x, a[x][0], a[x][1]);
-            attn_e4m3_f16(w.y, a[x][2], a[x][3]);
-          } else {
-            attn_e2m1_f16(*reinterpret_cast<const uint32_t*>(src + 16 * b + 4 * c), a[x]);
+        for (int u = 0; u < 2; ++u) {
+          uint32_t a[2][4];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint8_t* src = kt + (16 * u + r + 8 * x) * C::kKs;
+            if (kFp8) {
+              const uint2 w = *reinterpret_cast<const uint2*>(src + 32 * b + 8 * c);
+              attn_e4m3_f16(w.x, a[x][0], a[x][1]);
+              attn_e4m3_f16(w.y, a[x][2], a[x][3]);
+            } else {
+              attn_e2m1_f16(*reinterpret_cast<const uint32_t*>(src + 16 * b + 4 * c), a[x]);
+            }
+          }
+          const float k0 = fk[(16 * u + r) * kNB + b], k1 = fk[(16 * u + r + 8) * kNB + b];
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            attn_mma_f16(d, a[0][0], a[1][0], a[0][1], a[1][1], qf[t][b][0], qf[t][b][1]);
+            attn_mma_f16(d, a[0][2], a[1][2], a[0][3], a[1][3], qf[t][b][2], qf[t][b][3]);
+            s[u][t][0] = __fmaf_rn(d[0], k0, s[u][t][0]);
+            s[u][t][1] = __fmaf_rn(d[1], k0, s[u][t][1]);
+            s[u][t][2] = __fmaf_rn(d[2], k1, s[u][t][2]);
+            s[u][t][3] = __fmaf_rn(d[3], k1, s[u][t][3]);
           }
         }
-        const float k0 = fk[r * kNB + b], k1 = fk[(r + 8) * kNB + b];
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) {
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          attn_mma_f16(d, a[0][0], a[1][0], a[0][1], a[1][1], qf[t][b][0], qf[t][b][1]);
-          attn_mma_f16(d, a[0][2], a[1][2], a[0][3], a[1][3], qf[t][b][2], qf[t][b][3]);
-          s[t][0] = __fmaf_rn(d[0], k0, s[t][0]);
-          s[t][1] = __fmaf_rn(d[1], k0, s[t][1]);
-          s[t][2] = __fmaf_rn(d[2], k1, s[t][2]);
-          s[t][3] = __fmaf_rn(d[3], k1, s[t][3]);
-        }
       }
-      const bool see0 = __shfl_sync(0xffffffffu, rw[0], r) >= 0;
-      const bool see1 = __shfl_sync(0xffffffffu, rw[0], r + 8) >= 0;
-      const float e0 = fe[r], e1 = fe[r + 8];
-      __syncwarp();
-      copy_k(rw[kS], st);
       // ---- softmax over the tokens, for the columns 2c and 2c + 1
-      uint32_t pb[kNT][2];
+      const unsigned there = __ballot_sync(0xffffffffu, rw[0] >= 0);
+      float e[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        e[u][0] = fe[16 * u + r];
+        e[u][1] = fe[16 * u + r + 8];
+      }
+      uint32_t pb[2][kNT][2];
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
-        float x[4];
-        x[0] = see0 ? s[t][0] * cs[t][0] : -INFINITY;
-        x[1] = see0 ? s[t][1] * cs[t][1] : -INFINITY;
-        x[2] = see1 ? s[t][2] * cs[t][0] : -INFINITY;
-        x[3] = see1 ? s[t][3] * cs[t][1] : -INFINITY;
-        const float a0 = fmaxf(x[0], x[2]), a1 = fmaxf(x[1], x[3]);
-        const float b0 = fmaxf(x[0] + e0, x[2] + e1), b1 = fmaxf(x[1] + e0, x[3] + e1);
-        const bool up = a0 > m[t][0] + 8.0f || a1 > m[t][1] + 8.0f || b0 > mv[t][0] + 8.0f || b1 > mv[t][1] + 8.0f;
+        float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float& x = s[u][t][k];
+            x = there >> (16 * u + r + 8 * (k >> 1)) & 1u ? x * cs[t][k & 1] : -INFINITY;
+            top[k & 1] = fmaxf(top[k & 1], x);
+            topv[k & 1] = fmaxf(topv[k & 1], x + e[u][k >> 1]);
+          }
+        const bool up = top[0] > m[t][0] + 8.0f || top[1] > m[t][1] + 8.0f || topv[0] > mv[t][0] + 8.0f ||
+                        topv[1] > mv[t][1] + 8.0f;
         if (__any_sync(0xffffffffu, up)) {
-          float nm[2] = {a0, a1}, nv2[2] = {b0, b1};
+          float f[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
-              nm[k] = fmaxf(nm[k], __shfl_xor_sync(0xffffffffu, nm[k], d));
-              nv2[k] = fmaxf(nv2[k], __shfl_xor_sync(0xffffffffu, nv2[k], d));
+              top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
+              topv[k] = fmaxf(topv[k], __shfl_xor_sync(0xffffffffu, topv[k], d));
             }
-            nm[k] = fmaxf(m[t][k], nm[k]);
-            nv2[k] = fmaxf(mv[t][k], nv2[k]);
-            l[t][k] *= nm[k] == -INFINITY ? 1.0f : attn_exp2(m[t][k] - nm[k]);
-            m[t][k] = nm[k];
+            top[k] = fmaxf(m[t][k], top[k]);
+            topv[k] = fmaxf(mv[t][k], topv[k]);
+            l[t][k] *= top[k] == -INFINITY ? 1.0f : attn_exp2(m[t][k] - top[k]);
+            f[k] = topv[k] == -INFINITY ? 1.0f : attn_exp2(mv[t][k] - topv[k]);
+            m[t][k] = top[k];
+            mv[t][k] = topv[k];
           }
-          const float f0 = nv2[0] == -INFINITY ? 1.0f : attn_exp2(mv[t][0] - nv2[0]);
-          const float f1 = nv2[1] == -INFINITY ? 1.0f : attn_exp2(mv[t][1] - nv2[1]);
-          mv[t][0] = nv2[0];
-          mv[t][1] = nv2[1];
 #pragma unroll
           for (int i = 0; i < 2 * kNB; ++i) {
-            o[t][i][0] *= f0;
-            o[t][i][1] *= f1;
-            o[t][i][2] *= f0;
-            o[t][i][3] *= f1;
+            o[t][i][0] *= f[0];
+            o[t][i][1] *= f[1];
+            o[t][i][2] *= f[0];
+            o[t][i][3] *= f[1];
           }
         }
-        const float m0 = m[t][0] == -INFINITY ? 0.0f : m[t][0], m1 = m[t][1] == -INFINITY ? 0.0f : m[t][1];
-        const float v0 = mv[t][0] == -INFINITY ? 0.0f : mv[t][0], v1 = mv[t][1] == -INFINITY ? 0.0f : mv[t][1];
-        l[t][0] += attn_exp2(x[0] - m0) + attn_exp2(x[2] - m0);
-        l[t][1] += attn_exp2(x[1] - m1) + attn_exp2(x[3] - m1);
-        // weights in f16 (half a step 2^-11 of each); their sum l keeps fp32
-        pb[t][0] = attn_transpose8(attn_pack_f16(attn_exp2(x[0] + (e0 - v0)), attn_exp2(x[1] + (e0 - v1))));
-        pb[t][1] = attn_transpose8(attn_pack_f16(attn_exp2(x[2] + (e1 - v0)), attn_exp2(x[3] + (e1 - v1))));
+        float ms[2], vs[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          ms[k] = m[t][k] == -INFINITY ? 0.0f : m[t][k];
+          vs[k] = mv[t][k] == -INFINITY ? 0.0f : mv[t][k];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          l[t][0] += attn_exp2(s[u][t][0] - ms[0]) + attn_exp2(s[u][t][2] - ms[0]);
+          l[t][1] += attn_exp2(s[u][t][1] - ms[1]) + attn_exp2(s[u][t][3] - ms[1]);
+          // weights in f16 (half a step 2^-11 of each); their sum l keeps fp32
+          pb[u][t][0] = attn_transpose8(attn_pack_f16(attn_exp2(s[u][t][0] + (e[u][0] - vs[0])),
+                                                      attn_exp2(s[u][t][1] + (e[u][0] - vs[1]))));
+          pb[u][t][1] = attn_transpose8(attn_pack_f16(attn_exp2(s[u][t][2] + (e[u][1] - vs[0])),
+                                                      attn_exp2(s[u][t][3] + (e[u][1] - vs[1]))));
+        }
       }
       // ---- o^T += V^T P^T, a block at a time: lane r has channels 4 r .. 4 r + 3 of the block
-      attn_copy_wait<2 * kS - 1>();
-      __syncwarp();
 #pragma unroll
       for (int b = 0; b < kNB; ++b) {
         if (b >= p.nb) break;
-        const uint2 f = *reinterpret_cast<const uint2*>(fv + b * 16 + 4 * c);
-        uint32_t v[4][2];  // channel 4 r + k: tokens (2c, 2c + 1), (2c + 8, 2c + 9)
-        const uint8_t* src = vt + 2 * c * C::kVs;
-        if (kFp8) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(src + 8 * x * C::kVs + 32 * b + 4 * r);
-            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(src + (8 * x + 1) * C::kVs + 32 * b + 4 * r);
-            attn_e4m3_f16(__byte_perm(w0, w1, 0x5140), v[0][x], v[1][x]);
-            attn_e4m3_f16(__byte_perm(w0, w1, 0x7362), v[2][x], v[3][x]);
+        for (int u = 0; u < 2; ++u) {
+          const uint2 f = *reinterpret_cast<const uint2*>(fv + b * 32 + 16 * u + 4 * c);
+          uint32_t v[4][2];  // channel 4 r + k: tokens (2c, 2c + 1), (2c + 8, 2c + 9)
+          const uint8_t* src = vt + (16 * u + 2 * c) * C::kVs;
+          if (kFp8) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t w0 = *reinterpret_cast<const uint32_t*>(src + 8 * x * C::kVs + 32 * b + 4 * r);
+              const uint32_t w1 = *reinterpret_cast<const uint32_t*>(src + (8 * x + 1) * C::kVs + 32 * b + 4 * r);
+              attn_e4m3_f16(__byte_perm(w0, w1, 0x5140), v[0][x], v[1][x]);
+              attn_e4m3_f16(__byte_perm(w0, w1, 0x7362), v[2][x], v[3][x]);
+            }
+          } else {
+            // nibbles of the same channel side by side: even channels, odd channels
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              w[x] = *reinterpret_cast<const uint16_t*>(src + ((x & 1) + 8 * (x >> 1)) * C::kVs + 16 * b + 2 * r);
+            const uint32_t a = w[0] | w[2] << 16, d = w[1] | w[3] << 16;
+            uint32_t ev[4], od[4];
+            attn_e2m1_f16((a & 0x0F0F0F0Fu) | ((d << 4) & 0xF0F0F0F0u), ev);
+            attn_e2m1_f16(((a >> 4) & 0x0F0F0F0Fu) | (d & 0xF0F0F0F0u), od);
+            v[0][0] = ev[0];
+            v[2][0] = ev[1];
+            v[0][1] = ev[2];
+            v[2][1] = ev[3];
+            v[1][0] = od[0];
+            v[3][0] = od[1];
+            v[1][1] = od[2];
+            v[3][1] = od[3];
           }
-        } else {
-          // nibbles of the same channel side by side: even channels, odd channels
-          uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = *reinterpret_cast<const uint16_t*>(src + ((x & 1) + 8 * (x >> 1)) * C::kVs + 16 * b + 2 * r);
-          const uint32_t a = w[0] | w[2] << 16, d = w[1] | w[3] << 16;
-          uint32_t ev[4], od[4];
-          attn_e2m1_f16((a & 0x0F0F0F0Fu) | ((d << 4) & 0xF0F0F0F0u), ev);
-          attn_e2m1_f16(((a >> 4) & 0x0F0F0F0Fu) | (d & 0xF0F0F0F0u), od);
-          v[0][0] = ev[0];
-          v[2][0] = ev[1];
-          v[0][1] = ev[2];
-          v[2][1] = ev[3];
-          v[1][0] = od[0];
-          v[3][0] = od[1];
-          v[1][1] = od[2];
-          v[3][1] = od[3];
-        }
-#pragma unroll
-        for (int t = 0; t < kNT; ++t) {
-          const uint32_t q0 = attn_mul_f16x2(pb[t][0], f.x), q1 = attn_mul_f16x2(pb[t][1], f.y);
-          attn_mma_f16(o[t][2 * b], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
-          attn_mma_f16(o[t][2 * b + 1], v[2][0], v[3][0], v[2][1], v[3][1], q0, q1);
+          for (int t = 0; t < kNT; ++t) {
+            const uint32_t q0 = attn_mul_f16x2(pb[u][t][0], f.x), q1 = attn_mul_f16x2(pb[u][t][1], f.y);
+            attn_mma_f16(o[t][2 * b], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
+            attn_mma_f16(o[t][2 * b + 1], v[2][0], v[3][0], v[2][1], v[3][1], q0, q1);
+          }
         }
       }
       __syncwarp();
-      copy_v(rw[kS], st);
+      copy(rw[kS], st);
       if (++st == kS) st = 0;
 #pragma unroll
       for (int k = 0; k < kS; ++k) rw[k] = rw[k + 1];

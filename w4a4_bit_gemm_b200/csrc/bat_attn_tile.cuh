@@ -599,20 +599,21 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     bool ok = true;
     uint4 buf[2][kBatch];
 
-    // this thread's token of the chunk the run stands at: its place (-1: none), the table's entry
-    int j_ahead = -1, h_ahead = 0, page_ahead = 0;
+    // this thread's token of the chunk the run stands at: its offset in the page (-1: none), the table's entry
+    int off_ahead = -1, h_ahead = 0, page_ahead = 0;
     auto look = [&]() {
-      j_ahead = -1;
+      off_ahead = -1;
       if (run.left <= 0) return;
       const int idx = run.pl.chunk * 128 + my_tok;
       if (idx >= run.nv) return;
-      j_ahead = run.span.token(idx);
+      const int j = run.span.token(idx), pg = attn_page_of(p, j);
       h_ahead = run.pl.hu;
-      page_ahead = __ldg(p.table + static_cast<int64_t>(run.pl.b) * p.max_pages + attn_page_of(p, j_ahead));
+      page_ahead = __ldg(p.table + static_cast<int64_t>(run.pl.b) * p.max_pages + pg);
+      off_ahead = j - pg * p.page_size;
     };
     auto found = [&](bool& bad) -> int {
-      const int r = j_ahead >= 0 ? attn_row_at(p, page_ahead, j_ahead, h_ahead) : -1;
-      bad = j_ahead >= 0 && r < 0;
+      const int r = off_ahead >= 0 ? attn_row_at(p, page_ahead, off_ahead, h_ahead) : -1;
+      bad = off_ahead >= 0 && r < 0;
       return r;
     };
     uint32_t sc[kDP / 32];
