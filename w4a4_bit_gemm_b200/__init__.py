@@ -9,6 +9,7 @@ calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from dataclasses import dataclass
@@ -112,12 +113,13 @@ def declared_functions() -> list[str]:
 
 # ---------------------------------------------------------------- marshalling helpers
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream: Optional[torch.cuda.Stream]):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 # The library takes device pointers only: every tensor handed to it must live in GPU memory.
@@ -125,6 +127,12 @@ _DEVICE_TYPE = "cuda"
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None, device=None) -> torch.Tensor:
+    # the usual case first: a call's checks are a good part of a small call's time
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        d = t.device
+        if d.type == _DEVICE_TYPE and (device is None or d == device):
+            return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != _DEVICE_TYPE:
@@ -536,11 +544,9 @@ class KVCache:
         """Both buffers on `device` and large enough for num_slots x H x D (before any launch)."""
         if self.fmt not in _KV_FMT:
             raise ValueError(f"unknown KV format {self.fmt!r}")
-        f = _KV_FMT[self.fmt]
-        _need_bytes(self.codes, "cache.codes",
-                    lib().bat_kv_codes_bytes(self.num_slots, self.H, self.D, f), device)
-        _need_bytes(self.scales, "cache.scales",
-                    lib().bat_kv_scales_bytes(self.num_slots, self.H, self.D), device)
+        n = self.num_slots * self.H * self.D
+        _need_bytes(self.codes, "cache.codes", n if self.fmt == "mxfp8" else n // 2, device)
+        _need_bytes(self.scales, "cache.scales", n // 32, device)
         return self
 
 
@@ -593,12 +599,18 @@ def bat_kv_attention_workspace_bytes(T: int, Hq: int, H: int, D: int, max_q_len:
     return lib().bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len, 1 if has_q_factors else 0)
 
 
-def _scratch(nbytes: int, dev, stream) -> torch.Tensor:
-    """A workspace of this call alone, in the allocator's order on the stream that uses it."""
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(T, Hq, H, D, max_q_len, has_q_factors) -> int:
+    """bat_kv_attention_workspace_bytes, a function of its arguments alone."""
+    return bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len, has_q_factors)
+
+
+def _scratch(n: int, dev, stream, dtype=torch.uint8) -> torch.Tensor:
+    """A buffer of this call, in the allocator's order on the stream that uses it."""
     if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(n, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return torch.empty(n, dtype=dtype, device=dev)
 
 
 def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q_starts, page_size: int,
@@ -621,13 +633,13 @@ def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q
     dev = q.device
     if dev.type != _DEVICE_TYPE:
         raise ValueError("q must be a CUDA tensor")
-    if q.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16:
         raise ValueError(f"q must be torch.bfloat16, got {q.dtype}")
     s0, s1, s2 = q.stride()
     if s2 != 1 or (s1 != D and Hq > 1):
         raise ValueError("q's heads and channels must be contiguous (only the token stride is free)")
-    q_stride = s0 if T > 1 else max(s0, Hq * D)
-    if kcache.D != D or vcache.D != D or kcache.H != vcache.H or kcache.num_slots != vcache.num_slots:
+    H = kcache.H
+    if kcache.D != D or vcache.D != D or H != vcache.H or kcache.num_slots != vcache.num_slots:
         raise ValueError("the caches' shapes do not match each other and q")
     kcache.check(dev)
     vcache.check(dev)
@@ -648,24 +660,20 @@ def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q
     if lse is not None:
         _need(lse, torch.float32, "lse", (T, Hq), dev)
     _on_device(dev, stream)
-    need = bat_kv_attention_workspace_bytes(T, Hq, kcache.H, D, max_q_len, Aq is not None)
     if workspace is None:
-        workspace = _scratch(need, dev, stream)
-    _need(workspace, torch.uint8, "workspace", None, dev)
+        workspace = _scratch(_attention_bytes(T, Hq, H, D, max_q_len, Aq is not None), dev, stream)
+    else:
+        _need(workspace, torch.uint8, "workspace", None, dev)
     if out is None:
-        if stream is None:
-            out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-        else:
-            with torch.cuda.stream(stream):
-                out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
-    _need(out, torch.bfloat16, "out", (T, Hq, D), dev)
-    k, v = kcache.struct(), vcache.struct()
-    _check(lib().bat_kv_attention(_ptr(q), T, Hq, q_stride, ctypes.byref(k), ctypes.byref(v),
-                                  _ptr(page_table), B, max_pages, page_size, _ptr(kv_lens),
-                                  _ptr(q_starts), max_q_len, D ** -0.5 if scale is None else scale,
-                                  window, sinks, _ptr(Aq), sq, _ptr(Bq), _ptr(Ao), so, _ptr(Bo),
-                                  _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
-                                  _stream(stream)), "bat_kv_attention")
+        out = _scratch(T * Hq * D, dev, stream, torch.bfloat16).view(T, Hq, D)
+    else:
+        _need(out, torch.bfloat16, "out", (T, Hq, D), dev)
+    _check(lib().bat_kv_attention(
+        q.data_ptr(), T, Hq, s0 if T > 1 else max(s0, Hq * D), ctypes.byref(kcache.struct()),
+        ctypes.byref(vcache.struct()), page_table.data_ptr(), B, max_pages, page_size,
+        kv_lens.data_ptr(), q_starts.data_ptr(), max_q_len, D ** -0.5 if scale is None else scale, window,
+        sinks, _ptr(Aq), sq, _ptr(Bq), _ptr(Ao), so, _ptr(Bo), out.data_ptr(), _ptr(lse),
+        workspace.data_ptr(), workspace.numel(), _stream(stream)), "bat_kv_attention")
     return out
 
 
@@ -697,20 +705,21 @@ def bat_rmsnorm_quantize(X, weight, A=None, B=None, g_lo=None, g_hi=None,
         _need(residual, torch.bfloat16, "residual", (M, K), dev)
     _on_device(dev, stream)
     cls = MXFP8 if fmt == "mxfp8" else MXFP4
-    if stream is None:
-        Xq = cls.empty(M, K, dev) if Xq is None else Xq
-        if residual_out is None and residual is not None:
-            residual_out = torch.empty_like(residual)
-    else:
-        with torch.cuda.stream(stream):
-            Xq = cls.empty(M, K, dev) if Xq is None else Xq
-            if residual_out is None and residual is not None:
-                residual_out = torch.empty_like(residual)
-    if not isinstance(Xq, cls):
+    if Xq is None:
+        # codes and scales are both whole 16-byte pieces from the allocator
+        if M < 1 or K < 32 or K % 32:
+            raise ValueError(f"invalid {cls.__name__} shape rows={M} k={K}")
+        nb = (K + 127) // 128
+        Xq = cls(_scratch(M * K if fmt == "mxfp8" else M * K // 2, dev, stream),
+                 _scratch((M + 127) // 128 * nb * 512, dev, stream), M, K)
+    elif not isinstance(Xq, cls):
         raise TypeError(f"Xq must be an {cls.__name__} for fmt {fmt!r}")
-    Xq.check("Xq", dev)
+    else:
+        Xq.check("Xq", dev)
     if residual_out is not None:
         _need(residual_out, torch.bfloat16, "residual_out", (M, K), dev)
+    elif residual is not None:
+        residual_out = _scratch(M * K, dev, stream, torch.bfloat16).view(M, K)
     if y_out is not None:
         _need(y_out, torch.float32, "y_out", (M, K), dev)
     st = Xq.struct()
