@@ -782,21 +782,14 @@ namespace {
 
 template <int kX, bool kFp8>
 bat_status_t launch_norm(const bat::NormParams& p, int sms, cudaStream_t s) {
-  const int nvec = p.K / 8;
-  // few rows: one vector a thread (latency); many rows: two or more, in smaller CTAs of
-  // which several share an SM (while one waits for its sum another loads)
-  int v = nvec <= 512 ? 1 : (nvec <= 1024 ? 2 : 4);
-  if (p.M > 2 * sms && nvec > 256 && nvec <= 512) v = 2;
-  if (kX == 2 && v > 1) v = nvec <= 512 ? 1 : 0;  // these splits' coefficients leave no registers for more
-  int nt = v > 1 ? static_cast<int>(round_up((nvec + v - 1) / v, 32)) : 0;
-  if (p.K > bat::norm::kMaxCachedK) v = 0;
-  if (v <= 1) nt = v == 0 ? bat::norm::kMaxThreads : static_cast<int>(round_up(nvec < 64 ? 64 : nvec, 32));
-  constexpr int kTwo = kX == 2 ? 0 : 2, kFour = kX == 2 ? 0 : 4;
+  const int nvec = p.K / 16;
+  // one vector of 16 a thread up to 512 threads, then two; wider rows are read twice
+  const int v = nvec <= bat::norm::kMaxThreads ? 1 : (p.K <= bat::norm::kMaxCachedK ? 2 : 0);
+  const int nt = v == 0 ? bat::norm::kMaxThreads : static_cast<int>(round_up((nvec + v - 1) / v < 64 ? 64 : (nvec + v - 1) / v, 32));
   void (*k)(bat::NormParams) = v == 1   ? bat::bat_rmsnorm_quantize_kernel<1, kX, kFp8>
-                               : v == 2 ? bat::bat_rmsnorm_quantize_kernel<kTwo, kX, kFp8>
-                               : v == 4 ? bat::bat_rmsnorm_quantize_kernel<kFour, kX, kFp8>
+                               : v == 2 ? bat::bat_rmsnorm_quantize_kernel<2, kX, kFp8>
                                         : bat::bat_rmsnorm_quantize_kernel<0, kX, kFp8>;
-  const int64_t cap = static_cast<int64_t>(sms) * (nt <= 256 ? 4 : 2);
+  const int64_t cap = static_cast<int64_t>(sms) * (nt <= 512 ? 1024 / nt : 1);
   const unsigned grid = static_cast<unsigned>(p.M < cap ? p.M : cap);
   k<<<grid, nt, 0, s>>>(p);
   return cuda_status(cudaGetLastError());
