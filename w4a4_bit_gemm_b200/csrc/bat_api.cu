@@ -786,10 +786,11 @@ bat_status_t launch_norm(const bat::NormParams& p, int sms, cudaStream_t s) {
   // one vector of 16 a thread up to 512 threads, then two; wider rows are read twice
   const int v = nvec <= bat::norm::kMaxThreads ? 1 : (p.K <= bat::norm::kMaxCachedK ? 2 : 0);
   const int nt = v == 0 ? bat::norm::kMaxThreads : static_cast<int>(round_up((nvec + v - 1) / v < 64 ? 64 : (nvec + v - 1) / v, 32));
-  void (*k)(bat::NormParams) = v == 1   ? bat::bat_rmsnorm_quantize_kernel<1, kX, kFp8>
-                               : v == 2 ? bat::bat_rmsnorm_quantize_kernel<2, kX, kFp8>
-                                        : bat::bat_rmsnorm_quantize_kernel<0, kX, kFp8>;
-  const int64_t cap = static_cast<int64_t>(sms) * (nt <= 512 ? 1024 / nt : 1);
+  void (*k)(bat::NormParams) = v == 1 && nt <= 256 ? bat::bat_rmsnorm_quantize_kernel<1, kX, kFp8, 256>
+                               : v == 1            ? bat::bat_rmsnorm_quantize_kernel<1, kX, kFp8, 512>
+                               : v == 2            ? bat::bat_rmsnorm_quantize_kernel<2, kX, kFp8, 512>
+                                                   : bat::bat_rmsnorm_quantize_kernel<0, kX, kFp8, 512>;
+  const int64_t cap = static_cast<int64_t>(sms) * (nt <= 256 ? 512 / nt : 1);
   const unsigned grid = static_cast<unsigned>(p.M < cap ? p.M : cap);
   k<<<grid, nt, 0, s>>>(p);
   return cuda_status(cudaGetLastError());

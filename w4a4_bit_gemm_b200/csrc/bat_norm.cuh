@@ -249,8 +249,10 @@ __device__ __forceinline__ void norm_weight(const uint4 (&wv)[2], float (&h)[16]
 
 // kV > 0: the row's kV vectors of 16 a thread stay in registers (kV * 16 * blockDim.x >= K).
 // kV == 0: any K, the row is read once for the sum and once for the codes.
-template <int kV, int kX, bool kFp8>
-__global__ void __launch_bounds__(norm::kMaxThreads)
+// kThreads: the most threads a CTA is launched with; up to 256, two CTAs share an SM (three, at
+// 80 registers a thread, spill: 16384 x 4096 in 109 instead of 100 us).
+template <int kV, int kX, bool kFp8, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     bat_rmsnorm_quantize_kernel(const NormParams p) {
   __shared__ __align__(16) float sa[64];
   __shared__ float red[2][norm::kMaxThreads / 32];
