@@ -377,7 +377,7 @@ typedef struct {
  * rows or T * Hq), BAT_ERR_ALIGN, BAT_ERR_WORKSPACE, BAT_ERR_CUDA.
  */
 BAT_API size_t bat_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D,
-                                                int64_t max_q_len, int has_q_factors);
+                                                int64_t max_q_len);
 BAT_API bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride,
                                       const bat_kv_cache_t* K, const bat_kv_cache_t* V,
                                       const int32_t* page_table, int64_t B, int64_t max_pages,

@@ -83,7 +83,7 @@ def lib() -> ctypes.CDLL:
         "bat_kv_scales_bytes": (ctypes.c_size_t, [I64, I64, I64]),
         "bat_kv_quantize": (S, [P, I64, I64, I64, P, S, P, P, P, P, S, P, P, I64, P, P]),
         "bat_kv_dequantize": (S, [P, P, I64, I64, I64, S, P, I64, P, S, P, P, S, P]),
-        "bat_kv_attention_workspace_bytes": (Z, [I64, I64, I64, I64, I64, S]),
+        "bat_kv_attention_workspace_bytes": (Z, [I64, I64, I64, I64, I64]),
         "bat_kv_attention": (S, [P, I64, I64, I64, KP, KP, P, I64, I64, I64, P, P, I64, F, I64, I64,
                                  P, S, P, P, S, P, P, P, P, Z, P]),
         "bat_rmsnorm_quantize": (S, [P, P, P, I64, I64, F, P, S, P, P, P, S, SP, P, P, P]),
@@ -594,15 +594,14 @@ def bat_kv_dequantize(cache: KVCache, slots, A=None, B=None, out: Optional[torch
     return out
 
 
-def bat_kv_attention_workspace_bytes(T: int, Hq: int, H: int, D: int, max_q_len: int,
-                                     has_q_factors: bool = False) -> int:
-    return lib().bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len, 1 if has_q_factors else 0)
+def bat_kv_attention_workspace_bytes(T: int, Hq: int, H: int, D: int, max_q_len: int) -> int:
+    return lib().bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len)
 
 
 @functools.lru_cache(maxsize=256)
-def _attention_bytes(T, Hq, H, D, max_q_len, has_q_factors) -> int:
+def _attention_bytes(T, Hq, H, D, max_q_len) -> int:
     """bat_kv_attention_workspace_bytes, a function of its arguments alone."""
-    return bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len, has_q_factors)
+    return bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len)
 
 
 def _scratch(n: int, dev, stream, dtype=torch.uint8) -> torch.Tensor:
@@ -661,7 +660,7 @@ def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q
         _need(lse, torch.float32, "lse", (T, Hq), dev)
     _on_device(dev, stream)
     if workspace is None:
-        workspace = _scratch(_attention_bytes(T, Hq, H, D, max_q_len, Aq is not None), dev, stream)
+        workspace = _scratch(_attention_bytes(T, Hq, H, D, max_q_len), dev, stream)
     else:
         _need(workspace, torch.uint8, "workspace", None, dev)
     if out is None:

@@ -196,6 +196,21 @@ bool make_act_map(CUtensorMap* map, const void* x, int64_t rows, int64_t K) {
   return r == CUDA_SUCCESS;
 }
 
+// f16 rows [rows][D] for the attention tile kernel: box of 64 columns (128 bytes) x 128 rows,
+// 128-byte swizzle; columns past D and rows past the end read 0.
+bool make_rows16_map(CUtensorMap* map, const void* x, int64_t rows, int64_t D) {
+  EncodeTiledFn f = encode_fn();
+  if (!f) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D * 2)};
+  cuuint32_t box[2] = {64u, 128u};
+  cuuint32_t estr[2] = {1u, 1u};
+  CUresult r = f(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // ---------------------------------------------------------------- fp64 inverse (host)
 // Gauss-Jordan elimination with partial pivoting on an n x n row-major matrix.
 // Returns false if a pivot vanishes or the 1-norm condition number exceeds kMaxCond.
@@ -741,36 +756,35 @@ bat_status_t launch_attn_join(const bat::AttnParams& p, int dev, int bit, cudaSt
 }
 
 template <bool kFp8, int kDP>
-bat_status_t launch_attn_tile(bat::AttnParams& p, int dev, int sms, int bit, cudaStream_t s) {
+bat_status_t launch_attn_tile(bat::AttnParams& p, uint16_t* qt, int dev, int sms, int bit, cudaStream_t s) {
   using C = bat::attn_tile::Cfg<kDP>;
   auto k = bat::bat_attn_tile_kernel<kFp8, kDP>;
   bat_status_t st = attn_smem(k, dev, bit, C::kSmem);
   if (st != BAT_OK) return st;
   p.ctas = sms < kAttnTileCtas ? sms : kAttnTileCtas;
-  if (p.qa != nullptr) {
-    bat::AttnQRowsParams q = {};
-    q.q = p.q;
-    q.q_stride = p.q_stride;
-    q.a = p.qa;
-    q.b = p.qb;
-    q.out = const_cast<uint16_t*>(p.qt);
-    q.fac = const_cast<float*>(p.qt_fac);
-    q.rows = p.T * p.Hq;
-    q.Hq = p.Hq;
-    q.D = p.D;
-    q.nb = p.nb;
-    q.ls = p.qls;
-    q.sign = p.q_sign;
-    q.scale_log2 = p.scale_log2;
-    const int64_t want = (q.rows + 7) / 8, cap = static_cast<int64_t>(sms) * 5;
-    bat::bat_attn_q_rows_kernel<<<static_cast<unsigned>(want < cap ? want : cap), 256, 0, s>>>(q);
-    st = cuda_status(cudaGetLastError());
-    if (st != BAT_OK) return st;
-    st = launch_dependent(k, dim3(p.ctas), dim3(bat::attn_tile::kThreads), C::kSmem, s, p);
-  } else {
-    k<<<p.ctas, bat::attn_tile::kThreads, C::kSmem, s>>>(p);
-    st = cuda_status(cudaGetLastError());
-  }
+  CUtensorMap qmap;
+  if (!make_rows16_map(&qmap, qt, p.T * p.Hq, p.D)) return BAT_ERR_CUDA;
+  bat::AttnQRowsParams q = {};
+  q.q = p.q;
+  q.q_stride = p.q_stride;
+  q.a = p.qa;
+  q.b = p.qb;
+  q.out = qt;
+  q.fac = const_cast<float*>(p.qt_fac);
+  q.T = p.T;
+  q.Hq = p.Hq;
+  q.G = p.G;
+  q.D = p.D;
+  q.nb = p.nb;
+  q.ls = p.qls;
+  q.sign = p.q_sign;
+  q.scale_log2 = p.scale_log2;
+  const int64_t want = (p.T * p.Hq + 7) / 8, cap = static_cast<int64_t>(sms) * 8;
+  const size_t q_smem = (8 * 256 + (p.qa ? bat::attn_factor_floats(p.nb, p.qls) : 0)) * 4;
+  bat::bat_attn_q_rows_kernel<<<static_cast<unsigned>(want < cap ? want : cap), 256, q_smem, s>>>(q);
+  st = cuda_status(cudaGetLastError());
+  if (st != BAT_OK) return st;
+  st = launch_dependent(k, dim3(p.ctas), dim3(bat::attn_tile::kThreads), C::kSmem, s, p, qmap);
   if (st != BAT_OK) return st;
   return launch_attn_join<C::kRows>(p, dev, C::kRows == 256 ? 7 : 8, s);
 }
@@ -1104,12 +1118,12 @@ bat_status_t bat_kv_dequantize(const void* cache_codes, const void* cache_scales
 }
 
 size_t bat_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_t D,
-                                        int64_t max_q_len, int has_q_factors) {
+                                        int64_t max_q_len) {
   if (T < 1 || Hq < 1 || H < 1 || Hq % H != 0 || D < 32 || D % 32 != 0 || D > 256 || max_q_len < 1) return 0;
   if (T > kMaxRows / Hq) return 0;
   if (!attn_use_tile(Hq / H, max_q_len)) return attn_part_bytes(kAttnRowCtas, attn_row_unit(Hq / H, D), D);
   return attn_part_bytes(kAttnTileCtas, attn_tile_rows(D), D) +
-         (has_q_factors ? static_cast<size_t>(round_up(T * Hq * D * 2, 256) + round_up(T * Hq * 4, 256)) : 0);
+         static_cast<size_t>(round_up(T * Hq * D * 2, 256) + round_up(T * Hq * 4, 256));
 }
 
 bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride,
@@ -1144,7 +1158,7 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
       ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(kv_lens) |
         reinterpret_cast<uintptr_t>(q_starts) | reinterpret_cast<uintptr_t>(lse)) & 3u) != 0)
     return BAT_ERR_ALIGN;
-  const size_t need = bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len, Aq != nullptr);
+  const size_t need = bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len);
   if (!workspace || workspace_bytes < need) return BAT_ERR_WORKSPACE;
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return BAT_ERR_ALIGN;
   int dev = 0, sms = 0;
@@ -1205,15 +1219,13 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   p.marks = reinterpret_cast<bat::AttnMark*>(ws);
   ws += round_up(ctas * static_cast<int64_t>(sizeof(bat::AttnMark)), 256);
   if (tile) {
-    if (Aq) {
-      p.qt = reinterpret_cast<const uint16_t*>(ws);
-      p.qt_fac = reinterpret_cast<const float*>(ws + round_up(T * Hq * D * 2, 256));
-    }
+    uint16_t* qt = reinterpret_cast<uint16_t*>(ws);
+    p.qt_fac = reinterpret_cast<const float*>(ws + round_up(T * Hq * D * 2, 256));
     if (D > 128)
-      return fp8 ? launch_attn_tile<true, 256>(p, dev, sms, 9, s) : launch_attn_tile<false, 256>(p, dev, sms, 10, s);
+      return fp8 ? launch_attn_tile<true, 256>(p, qt, dev, sms, 9, s) : launch_attn_tile<false, 256>(p, qt, dev, sms, 10, s);
     if (D > 64)
-      return fp8 ? launch_attn_tile<true, 128>(p, dev, sms, 11, s) : launch_attn_tile<false, 128>(p, dev, sms, 12, s);
-    return fp8 ? launch_attn_tile<true, 64>(p, dev, sms, 13, s) : launch_attn_tile<false, 64>(p, dev, sms, 14, s);
+      return fp8 ? launch_attn_tile<true, 128>(p, qt, dev, sms, 11, s) : launch_attn_tile<false, 128>(p, qt, dev, sms, 12, s);
+    return fp8 ? launch_attn_tile<true, 64>(p, qt, dev, sms, 13, s) : launch_attn_tile<false, 64>(p, qt, dev, sms, 14, s);
   }
   // variants by the head's blocks (2, 4 or 8) and the unit's rows (8 or 16)
   if (D > 128)

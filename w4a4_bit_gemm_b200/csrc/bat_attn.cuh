@@ -83,8 +83,7 @@ struct AttnParams {
   int scale_words;         // the scale arrays may be read by 32-bit words (nb % 4 == 0, aligned)
   float scale_log2;        // |scale| * log2(e)
   float q_sign;            // sign of the scale, taken into q
-  const uint16_t* qt;      // tile kernel with P_q: f16 rows of q P_q (attn_q_rows), or null
-  const float* qt_fac;     // and their factors, [T][Hq]
+  const float* qt_fac;     // tile kernel: factors of the prepared q rows, [Hkv][T][G]
 };
 
 // One sequence's facts, from the device arrays, made safe: n >= 0, tokens inside [0, T),

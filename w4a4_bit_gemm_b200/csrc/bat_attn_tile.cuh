@@ -5,14 +5,21 @@
 // KV head: rows run over tokens and the group's heads, so grouped heads share every K and V
 // tile. Its visible tokens come in chunks of 128. Warp roles:
 //   warps 0-3, 4-7  softmax of tile 0 / 1, one row a thread: S from TMEM, weights back into
-//                   S's columns as the A operand of the second product; q staging and the output
-//   warps 8-15      K and V: page lookup, loads of codes and scales a chunk ahead, expansion
-//                   to f16 (K) and bf16 (V) in swizzled shared memory
+//                   S's columns as the A operand of the second product; the output
+//   warps 8-15      K and V: loads of codes a chunk ahead, expansion to f16 (K) and bf16 (V) in
+//                   swizzled shared memory, 16 tokens of a chunk each
 //   warp 16         issues the MMAs and owns TMEM
+//   warps 17, 18    page lookups, cache rows and the scales' factors of 64 tokens each, up to
+//                   three chunks ahead (done by the loader warps themselves these took a third of
+//                   their time)
+//   warp 19         q tiles by TMA, while the unit before is still in its last products
+// q comes from bat_attn_q_rows_kernel: f16 rows (times P_q) in the order [KV head][token][head of the
+// group], so that a tile's 128 rows lie together whatever the group's size.
 // Per chunk and tile: S = q K^T (M 128, N 128, K = D, kind::f16 on f16) and
 // o += P V (N = D, K = 128, kind::f16 on bf16, P from TMEM). The MMAs of one tile run while the
-// other tile's warps are in their softmax. The maximum is lazy: o is rescaled only when the
-// row's maximum grew by more than 2^8, which bf16 weights and fp32 sums hold without loss.
+// other tile's warps are in their softmax. The maximum is lazy: the scores go against a
+// reference that is within 2^40 below the row's maximum, which bf16 weights and fp32 sums hold without
+// loss, so S is read once and o hardly ever rescaled.
 // What bounds it: the tensor pipe and the exponentials' unit about equally (a chunk of 256
 // rows: 2048 cycles of MMA at the nominal rate, 2048 cycles of 16 exponentials a cycle).
 //
@@ -28,10 +35,12 @@ namespace bat {
 namespace attn_tile {
 constexpr int kPanelBytes = 128 * 128;  // 128 rows of 64 16-bit channels, 128-byte swizzle
 constexpr int kLoadWarps = 8;
-constexpr int kThreads = 640;  // 17 warps work; the register split goes by four warps
-constexpr int kRegsSoftmax = 120, kRegsLoad = 104, kRegsMma = 32;
-static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsMma <= 5 * 96, "the split stays within the launch's registers");
-constexpr int kInfo = 8;                // chunks whose notes are kept (see the ring's order)
+constexpr int kThreads = 640;  // the register split goes by four warps
+constexpr int kRegsSoftmax = 112, kRegsLoad = 104, kRegsOther = 48;
+static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsOther <= 5 * 96, "the split stays within the launch's registers");
+constexpr int kInfo = 8;                // chunks whose notes are kept
+// A note is overwritten eight chunks on, by a warp that is at most kSlots chunks ahead of the loaders,
+// and they at most kStages / 2 chunks ahead of the products whose softmax read it.
 
 template <int kDP>
 struct Cfg {
@@ -40,17 +49,29 @@ struct Cfg {
   static constexpr int kPanels = kDP / 64;
   static constexpr int kStageBytes = kPanels * kPanelBytes;
   static constexpr int kStages = kDP == 64 ? 8 : (kDP == 128 ? 4 : 2);
+  static constexpr int kSlots = kDP == 256 ? 2 : 3;  // chunks whose rows and factors are kept
+  static_assert(kSlots + kStages / 2 <= kInfo - 1, "notes outlive their readers");
   static constexpr int kQBytes = kTiles * kPanels * kPanelBytes;
   static constexpr int kSmem = 1024 + kQBytes + kStages * kStageBytes;  // dynamic, 1024 for alignment
 };
 }  // namespace attn_tile
 
-// What the loader notes about a chunk for the softmax warps.
+// What the loader warps note about a chunk for the softmax warps.
 struct AttnNote {
-  float kfac;         // 2^(largest K scale of the chunk)
-  int any;            // some token is hidden (bad page) or holds a NaN in V
+  float kfac[8];      // 2^(largest K scale of the warp's 16 tokens)
+  int any[8];         // some of its tokens are hidden (bad page) or hold a NaN in V
   uint32_t tok[128];  // bit 31: hidden; bit b: NaN in V's block b
 };
+// A chunk's cache rows (-1: none) and factors (16-bit pairs) for the loader warps.
+template <int kNB>
+struct AttnIndex {
+  int row[128];
+  uint32_t fac[2][128][kNB];  // K, V
+};
+__device__ __forceinline__ bool attn_note_any(const AttnNote& n) {
+  const volatile int4* a = reinterpret_cast<const volatile int4*>(n.any);
+  return (a[0].x | a[0].y | a[0].z | a[0].w | a[1].x | a[1].y | a[1].z | a[1].w) != 0;
+}
 
 // idesc of kind::f16, fp32 accumulation, A K-major; kBf16: both operands bf16, else f16;
 // kMnB: B is MN-major.
@@ -78,17 +99,27 @@ __device__ __forceinline__ bool attn_elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// Loader warps only: a barrier of their 256 threads that also agrees on `ok`, so that all of them
-// leave together after a wait that ran out.
-__device__ __forceinline__ bool attn_load_sync(bool ok) {
-  uint32_t r;
+// TMEM loads in flight: the wait names the registers, so that nothing uses them before it.
+__device__ __forceinline__ void attn_tmem_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// 16 columns, complete on return (the rare paths).
+__device__ __forceinline__ void attn_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 256, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(ok))
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
-  return r != 0;
 }
 
 // Channel order that the expansion of V leaves (see attn_e4m3_bits, attn_e2m1_bits): position
@@ -98,56 +129,74 @@ __host__ __device__ constexpr int attn_v_order(int i) {
   return kFp8 ? (i & ~3) | ((i & 1) << 1) | ((i >> 1) & 1) : (i & ~7) | ((i >> 1) & 3) | ((i & 1) << 2);
 }
 
-// Rows of q P_q in f16 with their factors, for units that many tiles share: warp a row.
+// Rows of q (P_q) in f16, times the power of two that brings the row's largest channel to
+// [2^14, 2^15), and the factor that takes it back; warp a row.
 struct AttnQRowsParams {
   const uint16_t* q;
   int64_t q_stride;
-  const float* a;
+  const float* a;  // factors of P_q, or null
   const float* b;
-  uint16_t* out;   // f16 [T][Hq][D]
-  float* fac;      // [T][Hq]
-  int64_t rows;    // T * Hq
-  int Hq, D, nb, ls;
+  uint16_t* out;   // f16 [Hkv][T][G][D]
+  float* fac;      // [Hkv][T][G]
+  int64_t T;
+  int Hq, G, D, nb, ls;
   float sign, scale_log2;
 };
 __global__ void __launch_bounds__(256) bat_attn_q_rows_kernel(const AttnQRowsParams p) {
-  __shared__ __align__(16) float sp[8 * 1024];
-  __shared__ __align__(16) float fac[kv::kFacFloats];
+  extern __shared__ __align__(16) float smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float* sx = smem + warp * 256;  // the row in fp32
   allow_dependents();
-  kv_build_p(sp, fac, p.a, p.b, p.nb, p.ls);
-  const int lane = threadIdx.x & 31, u = lane & 7;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < p.rows; row += step) {
+  AttnFactors f{nullptr, nullptr, 3};
+  if (p.a) {
+    f = attn_stage_factors(smem + 8 * 256, p.a, p.b, p.nb, p.ls);
+    __syncthreads();
+  }
+  const int64_t rows = p.T * p.Hq, step = static_cast<int64_t>(gridDim.x) * 8;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp; row < rows; row += step) {
     const int64_t t = row / p.Hq;
-    const uint16_t* src = p.q + t * p.q_stride + (row - t * p.Hq) * p.D;
-    float y[2][4], mx = 0.0f;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int blk = 4 * g + (lane >> 3);
-      const bool has = blk < p.nb;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
+    const int hq = static_cast<int>(row - t * p.Hq), h = hq / p.G;
+    const int64_t dst = (h * p.T + t) * p.G + (hq - h * p.G);
+    const bool has = 8 * lane < p.D;  // 8 channels a lane
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (has) w = *(reinterpret_cast<const uint4*>(p.q + t * p.q_stride + static_cast<int64_t>(hq) * p.D) + lane);
+    float x[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y), bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
+    if (p.a) {
       if (has) {
-        const uint2 w = *reinterpret_cast<const uint2*>(src + 32 * blk + 4 * u);
-        x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y); x[3] = bf16hi(w.y);
+        reinterpret_cast<float4*>(sx)[2 * lane] = make_float4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<float4*>(sx)[2 * lane + 1] = make_float4(x[4], x[5], x[6], x[7]);
       }
-      y[g][0] = y[g][1] = y[g][2] = y[g][3] = 0.0f;
-      if (4 * g < p.nb) kv_block_product(sp + (has ? blk : 0) * 1024, x, lane, y[g]);
-      if (!has) y[g][0] = y[g][1] = y[g][2] = y[g][3] = 0.0f;
+      __syncwarp();
+      float y[2][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fabsf(y[g][j]));
+      for (int g = 0; g < 2; ++g)
+        if (32 * g + lane < 8 * p.nb) attn_block_apply(f, (32 * g + lane) >> 3, sx + 32 * ((32 * g + lane) >> 3), lane & 7, y[g]);
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (32 * g + lane < 8 * p.nb)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sx[32 * ((32 * g + lane) >> 3) + 8 * j + (lane & 7)] = y[g][j];
+      __syncwarp();
+      if (has) {
+        const float4 a = reinterpret_cast<const float4*>(sx)[2 * lane], b = reinterpret_cast<const float4*>(sx)[2 * lane + 1];
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+      }
+      __syncwarp();
     }
+    float mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]));
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
     float down;
     const float up = attn_row_up(mx, down) * p.sign;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int blk = 4 * g + (lane >> 3);
-      if (blk < p.nb)
-        *reinterpret_cast<uint2*>(p.out + row * p.D + 32 * blk + 4 * u) =
-            make_uint2(attn_pack_f16(y[g][0] * up, y[g][1] * up), attn_pack_f16(y[g][2] * up, y[g][3] * up));
-    }
-    if (lane == 0) p.fac[row] = down * p.scale_log2;
+    if (has)
+      *(reinterpret_cast<uint4*>(p.out + dst * p.D) + lane) =
+          make_uint4(attn_pack_f16(x[0] * up, x[1] * up), attn_pack_f16(x[2] * up, x[3] * up),
+                     attn_pack_f16(x[4] * up, x[5] * up), attn_pack_f16(x[6] * up, x[7] * up));
+    if (lane == 0) p.fac[dst] = down * p.scale_log2;
   }
 }
 
@@ -158,14 +207,14 @@ struct AttnRun {
   AttnSeq seq;
   AttnSpan span;
   int nv;
-  int64_t left;  // chunks, this one among them
+  int left;  // chunks, this one among them (a CTA's run is below 2^31)
   __device__ __forceinline__ void enter(const AttnParams& p) {
     span = attn_tile_span<kTile>(p, seq, pl.tile);
     nv = span.count();
   }
   __device__ __forceinline__ void start(const AttnParams& p, const AttnPlace& place, int64_t n) {
     pl = place;
-    left = n;
+    left = static_cast<int>(n);
     if (left > 0) {
       seq = attn_seq(p, pl.b);
       enter(p);
@@ -185,8 +234,7 @@ struct AttnRun {
     enter(p);
   }
   __device__ __forceinline__ int chunks_here() const {
-    const int64_t n = pl.chunks - pl.chunk;
-    return static_cast<int>(n < left ? n : left);
+    return min(pl.chunks - pl.chunk, left);
   }
   // tiles of 128 rows that hold rows
   __device__ __forceinline__ int tiles(const AttnParams& p) const {
@@ -195,18 +243,17 @@ struct AttnRun {
 };
 
 template <bool kFp8, int kDP>
-__global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
+    const AttnParams p, const __grid_constant__ CUtensorMap qmap) {
   using C = attn_tile::Cfg<kDP>;
   constexpr int kTile = C::kRows, kStages = C::kStages;
   extern __shared__ __align__(16) uint8_t raw[];
-  __shared__ AttnNote notes[attn_tile::kInfo];
-  __shared__ int s_rows[2][128];
-  __shared__ uint8_t s_scale[2][2][128][kDP / 32];
-  __shared__ int s_top[2][4];
+  __shared__ __align__(16) AttnNote notes[attn_tile::kInfo];
+  __shared__ AttnIndex<kDP / 32> s_index[C::kSlots];
   __shared__ uint32_t s_nan[C::kRows][kDP / 32];  // written only where a NaN was seen
   __shared__ __align__(16) float s_oa[64];
   __shared__ __align__(16) float s_ob[kDP / 32 * 16];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 2 * 4 + 1];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 2 * 5 + 2 * C::kSlots + 1];
   __shared__ uint32_t s_tmem;
   __shared__ AttnPlace s_place;
   __shared__ int64_t s_run;
@@ -221,7 +268,10 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
   auto s_full = [&](int t) { return bars + 8 * (2 * kStages + 2 + t); };
   auto p_full = [&](int t) { return bars + 8 * (2 * kStages + 4 + t); };
   auto o_full = [&](int t) { return bars + 8 * (2 * kStages + 6 + t); };
-  const uint32_t drain = bars + 8 * (2 * kStages + 8);
+  auto q_free = [&](int t) { return bars + 8 * (2 * kStages + 8 + t); };
+  auto i_full = [&](int s) { return bars + 8 * (2 * kStages + 10 + s); };
+  auto i_empty = [&](int s) { return bars + 8 * (2 * kStages + 10 + C::kSlots + s); };
+  const uint32_t drain = bars + 8 * (2 * kStages + 10 + 2 * C::kSlots);
 
   allow_dependents();
   if (threadIdx.x == 0) {
@@ -230,10 +280,15 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
       mbar_init(empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full(t), 4);
+      mbar_init(q_full(t), 1);
+      mbar_init(q_free(t), 1);
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t), 4);
       mbar_init(o_full(t), 1);
+    }
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(i_full(i), 2);
+      mbar_init(i_empty(i), attn_tile::kLoadWarps);
     }
     mbar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -275,7 +330,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     uint32_t n_s = 0;  // chunks of this tile so far (phases of s_full, o_full)
     uint32_t n_c = 0;  // chunks of the run so far (the notes' ring)
     bool ok = t < C::kTiles;
-    grid_dependency_wait();  // the transformed q rows, where a kernel before this one writes them
+    grid_dependency_wait();  // the q rows' factors
     for (int seg = 0; ok && run.left > 0; ++seg) {
       const int n = run.chunks_here();
       if (t >= run.tiles(p)) {
@@ -283,54 +338,16 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
         n_c += n;
         continue;
       }
-      const int64_t row = static_cast<int64_t>(run.pl.tile) * kTile + 128 * t + rr;
-      const int64_t rt = row / p.G;
-      const bool valid = rt < run.seq.n;
-      const int64_t tok = run.seq.t0 + rt;
-      const int head = run.pl.hu * p.G + static_cast<int>(row - rt * p.G);
       const int base = run.seq.len - run.seq.n;
-      const int pos = valid ? base + static_cast<int>(rt) : -1;
-      // ---- q row to shared memory (read twice: for its largest channel, and converted)
-      float cs = 0.0f;
+      int pos;
+      float cs;
       {
-        const uint32_t qrow = q_base + (t * C::kPanels) * attn_tile::kPanelBytes + rr * 128;
-        const bool ready = p.qt != nullptr;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            ready ? p.qt + (tok * p.Hq + head) * p.D : p.q + tok * p.q_stride + static_cast<int64_t>(head) * p.D);
-        float up = 1.0f;
-        if (!ready) {
-          float mx = 0.0f;
-#pragma unroll 8
-          for (int v = 0; v < kDP / 8; ++v) {
-            const uint4 w = valid && 8 * v < p.D ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16lo(e[k])), fabsf(bf16hi(e[k]))));
-          }
-          float down;
-          up = attn_row_up(mx, down) * p.q_sign;
-          cs = down * p.scale_log2;
-        } else if (valid) {
-          cs = __ldg(p.qt_fac + tok * p.Hq + head);
-        }
-#pragma unroll 8
-        for (int v = 0; v < kDP / 8; ++v) {
-          uint4 w = valid && 8 * v < p.D ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
-          if (!ready) {
-            w.x = attn_pack_f16(bf16lo(w.x) * up, bf16hi(w.x) * up);
-            w.y = attn_pack_f16(bf16lo(w.y) * up, bf16hi(w.y) * up);
-            w.z = attn_pack_f16(bf16lo(w.z) * up, bf16hi(w.z) * up);
-            w.w = attn_pack_f16(bf16lo(w.w) * up, bf16hi(w.w) * up);
-          }
-          const uint32_t a = qrow + (v >> 3) * attn_tile::kPanelBytes + (((v & 7) ^ (rr & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
-                       : "memory");
-        }
+        const int64_t row = static_cast<int64_t>(run.pl.tile) * kTile + 128 * t + rr;
+        const int64_t rt = row / p.G;
+        const bool valid = rt < run.seq.n;
+        pos = valid ? base + static_cast<int>(rt) : -1;
+        cs = valid ? p.qt_fac[(run.pl.hu * p.T + run.seq.t0) * p.G + row] : 0.0f;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full(t));
-
       // the row's visible columns, as indices among the unit's visible tokens: [v_lo, v_hi) and
       // [0, v_sink)
       const AttnSpan sp = run.span;
@@ -385,21 +402,21 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
         if (!ok) break;
         tc_fence_after();
         // V of the chunk before is complete: its notes
-        if (i > 0 && *reinterpret_cast<volatile int*>(&notes[(n_c - 1) % attn_tile::kInfo].any)) see_nan(n_c - 1, chunk - 1);
+        if (i > 0 && attn_note_any(notes[(n_c - 1) % attn_tile::kInfo])) see_nan(n_c - 1, chunk - 1);
         const AttnNote& note = notes[n_c % attn_tile::kInfo];
-        const float cc = fmaxf(cs * note.kfac, 1e-37f);
+        // factor of 16 columns (their tokens share a loader warp)
+        auto cc = [&](int g) { return fmaxf(cs * note.kfac[g], 1e-37f); };
         const int i0 = chunk * 128;
-        // masked columns go to TMEM as -inf, so that the two passes below need no test (S is read
-        // twice, 32 columns at a time, instead of being held: 120 registers a thread do)
+        // masked columns go to TMEM as -inf, so that the pass below needs no test
         const bool whole = (i0 >= all_lo || i0 + 128 <= sp.ns) && i0 + 128 <= all_hi;
-        const bool hidden = *reinterpret_cast<const volatile int*>(&note.any) != 0;
+        const bool hidden = attn_note_any(note);
         if (!whole || hidden) {
           const int c_hi = v_hi - i0, c_lo = v_lo - i0, c_sink = v_sink - i0;
 #pragma unroll 1
           for (int k = 0; k < 128; k += 32) {
             uint32_t s[32];
             tmem_ld_32x32b_x32(s_col(t) + lane_base + k, s);
-            tmem_wait_ld();
+            attn_tmem_wait(s);
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int c = k + j;
@@ -411,64 +428,74 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
           }
           tmem_wait_st();
         }
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int k = 0; k < 128; k += 32) {
-          uint32_t s[32];
-          tmem_ld_32x32b_x32(s_col(t) + lane_base + k, s);
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[0]) : "f"(__uint_as_float(s[j])), "f"(__uint_as_float(s[j + 1])));
-            asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[1]) : "f"(__uint_as_float(s[j + 2])), "f"(__uint_as_float(s[j + 3])));
-          }
-        }
-        const float mn = fmaxf(mx[0], mx[1]) * cc;
-        if (i == 0) {
-          m = mn;
-        } else {
-          const bool grow = mn > m + 8.0f;
-          if (__any_sync(0xffffffffu, grow)) {
-            // o of the chunks before: all their MMAs are done
-            ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), (n_s - 1) & 1u, kErrWaitTmemFull));
-            if (!ok) break;
-            tc_fence_after();
-            const float al = grow ? attn_exp2(m - mn) : 1.0f;
-            if (grow) m = mn;
-            l0 *= al;
-            l1 *= al;
-            for (int d = 0; d < p.D; d += 32) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(o_col(t) + lane_base + d, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-              tmem_st_32x32b_x16(o_col(t) + lane_base + d, reinterpret_cast<const uint32_t(&)[16]>(o[0]));
-              tmem_st_32x32b_x16(o_col(t) + lane_base + d + 16, reinterpret_cast<const uint32_t(&)[16]>(o[16]));
-            }
-          }
-        }
-        const float ms = m == -INFINITY ? 0.0f : m;
-        const uint64_t c2 = pack2(cc, cc), m2 = pack2(-ms, -ms);
-        uint64_t sum2 = pack2(l0, l1);
-        // weights over the columns already read: S's columns 32 k .. give way to 16 k ..
+        // 32 columns at a time, once: scores against the reference m, weights (up to 2^40) into
+        // S's columns 16 k .. that are already read; the next columns are on their way meanwhile
+        uint32_t s[2][32];
+        tmem_ld_32x32b_x32(s_col(t) + lane_base, s[0]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t s[32], w[16];
-          tmem_ld_32x32b_x32(s_col(t) + lane_base + 32 * k, s);
-          tmem_wait_ld();
+          uint32_t(&x)[32] = s[k & 1];
+          const float c0 = cc(2 * k), c1 = cc(2 * k + 1);
+          attn_tmem_wait(x);
+          if (k < 3) tmem_ld_32x32b_x32(s_col(t) + lane_base + 32 * (k + 1), s[(k + 1) & 1]);
+          float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[16])};
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+#pragma unroll
+            for (int j = 16 * g + 1; j < 16 * g + 15; j += 2)
+              asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[g]) : "f"(__uint_as_float(x[j])), "f"(__uint_as_float(x[j + 1])));
+            mx[g] = fmaxf(mx[g], __uint_as_float(x[16 * g + 15]));
+          }
+          const float top = fmaxf(mx[0] * c0, mx[1] * c1);
+          const bool grow = m == -INFINITY ? top > -INFINITY : top > m + 40.0f;
+          if (__any_sync(0xffffffffu, grow)) {
+            // a new reference, a whole number, so that what is already there is scaled exactly
+            const float mn = grow ? ceilf(top) : m;
+            const float al = m == -INFINITY ? 1.0f : attn_exp2(m - mn);
+            m = mn;
+            l0 *= al;
+            l1 *= al;
+            if (i > 0) {
+              // o of the chunks before: all their MMAs are done
+              ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), (n_s - 1) & 1u, kErrWaitTmemFull)) && ok;
+              tc_fence_after();
+#pragma unroll 1
+              for (int d = 0; d < p.D; d += 16) {
+                uint32_t o[16];
+                attn_tmem_ld16(o_col(t) + lane_base + d, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                tmem_st_32x32b_x16(o_col(t) + lane_base + d, o);
+              }
+            }
+            tmem_wait_st();
+#pragma unroll 1
+            for (int d = 0; d < 16 * k; d += 16) {
+              uint32_t w[16];
+              attn_tmem_ld16(s_col(t) + lane_base + d, w);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) w[j] = attn_mul_bf16x2(w[j], attn_pack(al, al));
+              tmem_st_32x32b_x16(s_col(t) + lane_base + d, w);
+            }
+          }
+          const float ms = m == -INFINITY ? 0.0f : m;
+          const uint64_t m2 = pack2(-ms, -ms);
+          uint64_t sum2 = pack2(l0, l1);
+          uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float a, b;
-            unpack2(ffma2(pack2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, m2), a, b);
+            const float cg = j < 8 ? c0 : c1;
+            unpack2(ffma2(pack2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), pack2(cg, cg), m2), a, b);
             a = attn_exp2(a);
             b = attn_exp2(b);
             sum2 = fadd2(sum2, pack2(a, b));
             w[j] = attn_pack(a, b);  // bf16: off by half a step 2^-8 of each weight, unbiased
           }
+          unpack2(sum2, l0, l1);
           tmem_st_32x32b_x16(s_col(t) + lane_base + 16 * k, w);
         }
-        unpack2(sum2, l0, l1);
+        if (!ok) break;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -479,7 +506,12 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
       ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), (n_s - 1) & 1u, kErrWaitTmemFull));
       if (!ok) break;
       tc_fence_after();
-      if (*reinterpret_cast<volatile int*>(&notes[(n_c - 1) % attn_tile::kInfo].any)) see_nan(n_c - 1, run.pl.chunk + n - 1);
+      if (attn_note_any(notes[(n_c - 1) % attn_tile::kInfo])) see_nan(n_c - 1, run.pl.chunk + n - 1);
+      const int64_t row = static_cast<int64_t>(run.pl.tile) * kTile + 128 * t + rr;
+      const int64_t rt = row / p.G;
+      const bool valid = rt < run.seq.n;
+      const int64_t tok = run.seq.t0 + rt;
+      const int head = run.pl.hu * p.G + static_cast<int>(row - rt * p.G);
       const float l = l0 + l1;
       const bool part = !(run.pl.chunk == 0 && n == run.pl.chunks);
       const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (seg == 0 ? 0 : 1)) * kTile + 128 * t + rr;
@@ -585,8 +617,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     static_assert(kTasks >= 1 && 16 % kTpi == 0, "a warp's tokens are whole load instructions");
     constexpr int kBatch = kTasks < 4 ? kTasks : 4;
     constexpr int kNB = kTasks / kBatch;                 // batches a tile: 1 or 2
-    const int lw = warp - 8, tid = threadIdx.x - 256;
-    const int my_tok = tid & 127, my_kv = tid >> 7;      // token and side (K or V) of this thread's lookups
+    const int lw = warp - 8;
     const int row_bytes = kFp8 ? p.D : p.D / 2;
     // the lanes of a quarter-warp take the pieces of one panel of neighbouring tokens, so that
     // their 16-byte stores fall on different banks of the swizzled rows
@@ -594,55 +625,13 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     const int piece = ((lane >> 3) % C::kPanels) * kPp + lane % kPp;
     const int sub = (lane >> 3) / C::kPanels * (8 / kPp) + lane % 8 / kPp;
     const bool has = piece * 16 < row_bytes;
-    const int pblk = kFp8 ? piece >> 1 : piece;          // its 32-channel block
-    const uint8_t* my_scales = my_kv ? p.v_scales : p.k_scales;
+    const int pblk = has ? (kFp8 ? piece >> 1 : piece) : 0;  // its 32-channel block
     bool ok = true;
     uint4 buf[2][kBatch];
-
-    // this thread's token of the chunk the run stands at: its offset in the page (-1: none), the table's entry
-    int off_ahead = -1, h_ahead = 0, page_ahead = 0;
-    auto look = [&]() {
-      off_ahead = -1;
-      if (run.left <= 0) return;
-      const int idx = run.pl.chunk * 128 + my_tok;
-      if (idx >= run.nv) return;
-      const int j = run.span.token(idx), pg = attn_page_of(p, j);
-      h_ahead = run.pl.hu;
-      page_ahead = __ldg(p.table + static_cast<int64_t>(run.pl.b) * p.max_pages + pg);
-      off_ahead = j - pg * p.page_size;
-    };
-    auto found = [&](bool& bad) -> int {
-      const int r = off_ahead >= 0 ? attn_row_at(p, page_ahead, off_ahead, h_ahead) : -1;
-      bad = off_ahead >= 0 && r < 0;
-      return r;
-    };
-    uint32_t sc[kDP / 32];
-    auto load_scales = [&](int row) {
-#pragma unroll
-      for (int b = 0; b < kDP / 32; ++b)
-        sc[b] = row >= 0 && b < p.nb ? __ldg(my_scales + static_cast<int64_t>(row) * p.nb + b) : 0u;
-    };
-    // scales, the largest of K's, and the notes of chunk c (parity c & 1), before a barrier
-    auto publish = [&](uint32_t c, bool bad) {
-      int top = 0;
-#pragma unroll
-      for (int b = 0; b < kDP / 32; ++b) {
-        s_scale[c & 1][my_kv][my_tok][b] = static_cast<uint8_t>(sc[b]);
-        // NaN scales stand for themselves and do not set the common scale
-        if (sc[b] != 255u) top = max(top, static_cast<int>(sc[b]));
-      }
-      if (my_kv == 0) {
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) s_top[c & 1][lw] = top;
-        AttnNote& nt = notes[c % attn_tile::kInfo];
-        nt.tok[my_tok] = bad ? 0x80000000u : 0u;
-        if (tid == 0) nt.any = 0;
-      }
-    };
-    auto load_batch = [&](int par, const uint8_t* codes, int b, uint4 (&dst)[kBatch]) {
+    auto load_batch = [&](const AttnIndex<kDP / 32>& ix, const uint8_t* codes, int b, uint4 (&dst)[kBatch]) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int row = s_rows[par][16 * lw + (b * kBatch + k) * kTpi + sub];
+        const int row = ix.row[16 * lw + (b * kBatch + k) * kTpi + sub];
         dst[k] = row >= 0 && has
                      ? __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(row) * row_bytes) + piece)
                      : make_uint4(0u, 0u, 0u, 0u);
@@ -660,59 +649,44 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
                      : "memory");
       }
     };
-
-    bool bad_now = false, bad_next = false;
-    {
-      look();
-      const int row = found(bad_now);
-      run.next_chunk(p);
-      look();
-      if (my_kv == 0) s_rows[0][my_tok] = row;
-      load_scales(row);
-      publish(0, bad_now);
-      ok = attn_load_sync(true);
-      load_batch(0, p.k_codes, 0, buf[0]);
-      if (kNB == 2)
-        load_batch(0, p.k_codes, kNB - 1, buf[1]);
-      else
-        load_batch(0, p.v_codes, 0, buf[1]);
+    const int total = run.left;
+    auto index_wait = [&](uint32_t c) {
+      ok = __all_sync(0xffffffffu, mbar_wait(i_full(c % C::kSlots), (c / C::kSlots) & 1u, kErrWaitFull)) && ok;
+    };
+    if (total > 0) {
+      index_wait(0);
+      if (ok) {
+        load_batch(s_index[0], p.k_codes, 0, buf[0]);
+        if (kNB == 2)
+          load_batch(s_index[0], p.k_codes, kNB - 1, buf[1]);
+        else
+          load_batch(s_index[0], p.v_codes, 0, buf[1]);
+      }
     }
-    const int64_t total = s_run;
     uint32_t el = 0;  // tiles put so far (K and V in turn)
-    for (int64_t c64 = 0; ok && c64 < total; ++c64) {
-      const uint32_t c = static_cast<uint32_t>(c64);
-      const int par = c & 1;
-      // rows and scales of the next chunk, the table's entries of the one after
-      const int row_next = found(bad_next);
-      if (my_kv == 0) s_rows[par ^ 1][my_tok] = row_next;
-      load_scales(row_next);
-      run.next_chunk(p);
-      look();
-      if (!(ok = attn_load_sync(ok))) break;
-
-      const int top = max(max(s_top[par][0], s_top[par][1]), max(s_top[par][2], s_top[par][3]));
+    for (uint32_t c = 0; ok && static_cast<int>(c) < total; ++c) {
+      const AttnIndex<kDP / 32>& ix = s_index[c % C::kSlots];
+      const AttnIndex<kDP / 32>& ix_next = s_index[(c + 1) % C::kSlots];
+      const bool more = static_cast<int>(c) + 1 < total;
       AttnNote& note = notes[c % attn_tile::kInfo];
-      if (tid == 0) note.kfac = attn_scale_value(top);
-      if (bad_now && my_kv == 0) note.any = 1;
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++el) {
         const uint32_t sidx = el % kStages;
         const uint32_t stage = st_base + sidx * C::kStageBytes;
-        ok = mbar_wait(empty(sidx), ((el / kStages) & 1u) ^ 1u, kErrWaitEmpty) && ok;
+        ok = __all_sync(0xffffffffu, mbar_wait(empty(sidx), ((el / kStages) & 1u) ^ 1u, kErrWaitEmpty)) && ok;
 #pragma unroll
         for (int b = 0; b < kNB; ++b) {
           constexpr int kSeq = 2 * kNB;
           const int e = kv * kNB + b;
-          uint4(&src)[kBatch] = buf[e & 1];
+            uint4(&src)[kBatch] = buf[e & 1];
           uint32_t nan = 0u;  // some byte's bit 7: a NaN among the batch's V codes
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             const int tk = 16 * lw + (b * kBatch + k) * kTpi + sub;
             const uint32_t w[4] = {src[k].x, src[k].y, src[k].z, src[k].w};
-            const uint32_t sb = has ? s_scale[par][kv][tk][pblk] : 0u;
+            const uint32_t f = ix.fac[kv][tk][pblk];
             uint32_t x[kX];
             if (kv == 0) {
-              const uint32_t f = sb == 255u ? 0x7E007E00u : attn_f16_pow2(top - static_cast<int>(sb));
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (kFp8)
@@ -723,8 +697,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
 #pragma unroll
               for (int q = 0; q < kX; ++q) x[q] = attn_mul_f16x2(x[q], f);
             } else {
-              const uint32_t f = attn_scale_pair<kFp8>(sb);
-              if ((f & 0x7FFFu) == 0x7FFFu) nan = 0x80u;
+              if (f == 0x7FFF7FFFu) nan = 0x80u;
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (kFp8) {
@@ -746,8 +719,8 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
             for (int k = 0; k < kBatch; ++k) {
               const int tk = 16 * lw + (b * kBatch + k) * kTpi + sub;
               const uint32_t w[4] = {src[k].x, src[k].y, src[k].z, src[k].w};
-              const uint32_t f = attn_scale_pair<kFp8>(has ? s_scale[par][1][tk][pblk] : 0u);
-              const bool all = (f & 0x7FFFu) == 0x7FFFu;
+              const uint32_t f = ix.fac[1][tk][pblk];
+              const bool all = f == 0x7FFF7FFFu;
               uint32_t x[kX], any = 0u;
 #pragma unroll
               for (int q = 0; q < kX; ++q) x[q] = 0u;
@@ -764,27 +737,30 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
               }
               if (any != 0u || all) {
                 put(stage, tk, x);
-                atomicOr(&note.tok[tk], 1u << pblk);
-                note.any = 1;
+                if (has) {
+                  atomicOr(&note.tok[tk], 1u << pblk);
+                  note.any[lw] = 1;
+                }
               }
             }
           }
           // the batch two steps on
           const int e2 = e + 2;
-          const int nxt = e2 >= kSeq ? 1 : 0, e3 = nxt ? e2 - kSeq : e2;
-          load_batch(par ^ nxt, e3 < kNB ? p.k_codes : p.v_codes, e3 % kNB, src);
+          const int e3 = e2 >= kSeq ? e2 - kSeq : e2;
+          if (e2 == kSeq && more) index_wait(c + 1);
+          if (ok && (e2 < kSeq || more)) load_batch(e2 >= kSeq ? ix_next : ix, e3 < kNB ? p.k_codes : p.v_codes, e3 % kNB, src);
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full(sidx));
+        if (lane == 0) {
+          mbar_arrive(full(sidx));
+          if (kv == 1) mbar_arrive(i_empty(c % C::kSlots));
+        }
       }
-      publish(c + 1, bad_next);
-      bad_now = bad_next;
-      if (!(ok = attn_load_sync(ok))) break;
     }
   } else {
     // ================================================================ MMA
-    setmaxnreg_dec<attn_tile::kRegsMma>();
+    setmaxnreg_dec<attn_tile::kRegsOther>();
     // the whole warp walks the runs and waits; one elected lane issues
     if (warp == 16) {
     const uint32_t id_s = attn_idesc<false, false>(128), id_o = attn_idesc<true, true>(p.D);
@@ -822,6 +798,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
         wait(q_full(t), n_q[t]++ & 1u, kErrWaitFull);
         if (t == 0) wait(full(k0), (el / kStages) & 1u, kErrWaitFull);
         if (ok) issue_s(t, k0);
+        if (ok && n == 1) commit(q_free(t));
       }
       if (!ok) break;
       commit(empty(k0));
@@ -846,6 +823,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
           if (more) {
             if (t == 0) wait(full(kst), kph, kErrWaitFull);
             if (ok) issue_s(t, kst);
+            if (ok && i + 2 == n) commit(q_free(t));  // the unit's last use of q
           }
         }
         if (!ok) break;
@@ -859,7 +837,130 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(c
     commit(drain);
     mbar_wait(drain, 0, kErrWaitTmemFull);
     __syncwarp();
+    } else if (warp < 19) {
+      // ============================================================== rows and factors
+      // Three steps a chunk, each on the loads of the step before in the chunk before: the table's
+      // entries, the rows and their scales, the factors.
+      constexpr int kW = (kDP / 32 + 3) / 4;
+      const int tk0 = 64 * (warp - 17) + lane;  // this lane's tokens: tk0 and tk0 + 32
+      int off[2] = {-1, -1}, page[2] = {0, 0}, h_ahead = 0;
+      uint32_t sck[2][kW], scv[2][kW];
+      bool bad[2] = {false, false}, ok = true;
+      const int total = run.left;
+      auto look = [&]() {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          off[x] = -1;
+          const int idx = run.pl.chunk * 128 + tk0 + 32 * x;
+          if (run.left <= 0 || idx >= run.nv) continue;
+          const int j = run.span.token(idx), pg = attn_page_of(p, j);
+          page[x] = __ldg(p.table + static_cast<int64_t>(run.pl.b) * p.max_pages + pg);
+          off[x] = j - pg * p.page_size;
+        }
+        h_ahead = run.pl.hu;
+        run.next_chunk(p);
+      };
+      auto load_scales = [&](const uint8_t* scales, int row, uint32_t (&sc)[kW]) {
+        const uint8_t* src = scales + static_cast<int64_t>(max(row, 0)) * p.nb;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          sc[w] = 0u;
+          if (row < 0) continue;
+          if (p.scale_words) {
+            if (4 * w < p.nb) sc[w] = __ldg(reinterpret_cast<const uint32_t*>(src) + w);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (4 * w + k < p.nb) sc[w] |= static_cast<uint32_t>(__ldg(src + 4 * w + k)) << (8 * k);
+          }
+        }
+      };
+      look();
+      for (int c = 0; ok && c <= total; ++c) {
+        int row[2] = {-1, -1};
+        bool hide[2] = {false, false};
+        if (c < total) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            row[x] = off[x] >= 0 ? attn_row_at(p, page[x], off[x], h_ahead) : -1;
+            hide[x] = off[x] >= 0 && row[x] < 0;
+          }
+          look();
+        }
+        if (c > 0) {
+          // factors and notes of chunk c - 1
+          const int at = c - 1;
+          AttnIndex<kDP / 32>& ix = s_index[at % C::kSlots];
+          AttnNote& nt = notes[at % attn_tile::kInfo];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int tk = tk0 + 32 * x;
+            int top = 0;
+#pragma unroll
+            for (int b = 0; b < kDP / 32; ++b) {
+              const int e = (sck[x][b / 4] >> (8 * (b & 3))) & 255;
+              top = e != 255 ? max(top, e) : top;  // NaN scales do not set the common scale
+            }
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+            for (int b = 0; b < kDP / 32; ++b) {
+              const int ek = (sck[x][b / 4] >> (8 * (b & 3))) & 255, ev = (scv[x][b / 4] >> (8 * (b & 3))) & 255;
+              ix.fac[0][tk][b] = ek == 255 ? 0x7E007E00u : attn_f16_pow2(top - ek);
+              ix.fac[1][tk][b] = attn_scale_pair<kFp8>(ev);
+            }
+            nt.tok[tk] = bad[x] ? 0x80000000u : 0u;
+            const unsigned any = __ballot_sync(0xffffffffu, bad[x]);
+            if ((lane & 15) == 0) {
+              nt.kfac[tk >> 4] = attn_scale_value(top);
+              nt.any[tk >> 4] = (any >> (lane & 16) & 0xFFFFu) != 0u;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(i_full(at % C::kSlots));
+        }
+        if (c < total) {
+          const int slot = c % C::kSlots;
+          ok = __all_sync(0xffffffffu, mbar_wait(i_empty(slot), ((c / C::kSlots) & 1u) ^ 1u, kErrWaitEmpty));
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            s_index[slot].row[tk0 + 32 * x] = row[x];
+            load_scales(p.k_scales, row[x], sck[x]);
+            load_scales(p.v_scales, row[x], scv[x]);
+            bad[x] = hide[x];
+          }
+        }
+      }
+    } else {
+      // ============================================================== q tiles
+      uint32_t n_q[2] = {0u, 0u};
+      bool ok = true;
+      grid_dependency_wait();  // the q rows
+      while (ok && run.left > 0) {
+        const int tiles = C::kTiles == 1 ? 1 : run.tiles(p);
+        for (int t = 0; ok && t < tiles; ++t) {
+          ok = __all_sync(0xffffffffu, mbar_wait(q_free(t), (n_q[t] & 1u) ^ 1u, kErrWaitEmpty));
+          if (!ok) break;
+          ++n_q[t];
+          // (rows past the sequence's end are other sequences' or past the tensor, read as 0: their
+          // scores are not used)
+          if (attn_elect()) {
+            const int64_t row0 = (run.pl.hu * p.T + run.seq.t0) * p.G + static_cast<int64_t>(run.pl.tile) * kTile + 128 * t;
+            mbar_expect_tx(q_full(t), C::kPanels * attn_tile::kPanelBytes);
+#pragma unroll
+            for (int k = 0; k < C::kPanels; ++k)
+              tma_load_2d(q_base + (t * C::kPanels + k) * attn_tile::kPanelBytes, &qmap, q_full(t), 64 * k,
+                          static_cast<int32_t>(row0));
+          }
+          __syncwarp();
+        }
+        run.next_unit(p, run.chunks_here());
+      }
+      // copies in flight land before the CTA's shared memory goes
+      for (int t = 0; t < C::kTiles; ++t)
+        if (n_q[t]) mbar_wait(q_full(t), (n_q[t] - 1) & 1u, kErrWaitFull);
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
