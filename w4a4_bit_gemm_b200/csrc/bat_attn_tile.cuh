@@ -429,15 +429,14 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
           tmem_wait_st();
         }
         // 32 columns at a time, once: scores against the reference m, weights (up to 2^40) into
-        // S's columns 16 k .. that are already read; the next columns are on their way meanwhile
-        uint32_t s[2][32];
-        tmem_ld_32x32b_x32(s_col(t) + lane_base, s[0]);
-#pragma unroll
+        // S's columns 16 k .. that are already read. (Not unrolled: the instruction caches hold the
+        // roles' loops then.)
+#pragma unroll 1
         for (int k = 0; k < 4; ++k) {
-          uint32_t(&x)[32] = s[k & 1];
+          uint32_t x[32];
+          tmem_ld_32x32b_x32(s_col(t) + lane_base + 32 * k, x);
           const float c0 = cc(2 * k), c1 = cc(2 * k + 1);
           attn_tmem_wait(x);
-          if (k < 3) tmem_ld_32x32b_x32(s_col(t) + lane_base + 32 * (k + 1), s[(k + 1) & 1]);
           float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[16])};
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
