@@ -62,10 +62,10 @@ struct AttnNote {
   int any[8];         // some of its tokens are hidden (bad page) or hold a NaN in V
   uint32_t tok[128];  // bit 31: hidden; bit b: NaN in V's block b
 };
-// A chunk's cache rows (-1: none) and factors (16-bit pairs) for the loader warps.
+// A chunk's cache rows (0 for none) and factors (16-bit pairs) for the loader warps.
 template <int kNB>
 struct AttnIndex {
-  int row[128];
+  uint32_t row[128];
   uint32_t fac[2][128][kNB];  // K, V
 };
 __device__ __forceinline__ bool attn_note_any(const AttnNote& n) {
@@ -627,22 +627,27 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
     const int pblk = has ? (kFp8 ? piece >> 1 : piece) : 0;  // its 32-channel block
     bool ok = true;
     uint4 buf[2][kBatch];
+    // (tokens that are not there read row 0, lanes past the head's channels its first piece: K's
+    // scores of such tokens are masked, V's weights are 0, the pieces are not stored)
+    const uint32_t piece_off = has ? 16u * piece : 0u;
     auto load_batch = [&](const AttnIndex<kDP / 32>& ix, const uint8_t* codes, int b, uint4 (&dst)[kBatch]) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int row = ix.row[16 * lw + (b * kBatch + k) * kTpi + sub];
-        dst[k] = row >= 0 && has
-                     ? __ldg(reinterpret_cast<const uint4*>(codes + static_cast<int64_t>(row) * row_bytes) + piece)
-                     : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t row = ix.row[16 * lw + (b * kBatch + k) * kTpi + sub];
+        dst[k] = __ldg(reinterpret_cast<const uint4*>(codes + piece_off + static_cast<uint64_t>(row) * static_cast<uint32_t>(row_bytes)));
       }
     };
     constexpr int kX = kFp8 ? 8 : 16;  // words a piece expands to
-    auto put = [&](uint32_t stage, int tk, const uint32_t (&x)[kX]) {
+    // shared-memory place of this lane's piece of its token k of a batch: token 16 lw + k kTpi + sub,
+    // 8-channel groups kX / 4 piece + u; k kTpi and sub share no bits, so the swizzle's exclusive or
+    // splits
+    const uint32_t put_row = (16 * lw + sub) * 128 + (kX / 4 * piece >> 3) * attn_tile::kPanelBytes;
+    const uint32_t put_unit = ((kX / 4 * piece & 7) ^ (sub & 7)) << 4;
+    auto put = [&](uint32_t stage, int k, const uint32_t (&x)[kX]) {
       if (!has) return;
 #pragma unroll
       for (int u = 0; u < kX / 4; ++u) {
-        const int unit = kX / 4 * piece + u;  // 8-channel group of the token's row
-        const uint32_t at = stage + (unit >> 3) * attn_tile::kPanelBytes + tk * 128 + (((unit & 7) ^ (tk & 7)) << 4);
+        const uint32_t at = stage + put_row + k * kTpi * 128 + (put_unit ^ (((k * kTpi & 7) ^ u) << 4));
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[4 * u]), "r"(x[4 * u + 1]),
                      "r"(x[4 * u + 2]), "r"(x[4 * u + 3])
                      : "memory");
@@ -710,7 +715,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
                 }
               }
             }
-            put(stage, tk, x);
+            put(stage, b * kBatch + k, x);
           }
           if (kv == 1 && (nan & 0x80808080u) != 0u) {
             // the rare way round: the pieces with a NaN again, with 0 in its place, and a note
@@ -735,7 +740,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
                 }
               }
               if (any != 0u || all) {
-                put(stage, tk, x);
+                put(stage, b * kBatch + k, x);
                 if (has) {
                   atomicOr(&note.tok[tk], 1u << pblk);
                   note.any[lw] = 1;
@@ -923,7 +928,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
           ok = __all_sync(0xffffffffu, mbar_wait(i_empty(slot), ((c / C::kSlots) & 1u) ^ 1u, kErrWaitEmpty));
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            s_index[slot].row[tk0 + 32 * x] = row[x];
+            s_index[slot].row[tk0 + 32 * x] = max(row[x], 0);
             load_scales(p.k_scales, row[x], sck[x]);
             load_scales(p.v_scales, row[x], scv[x]);
             bad[x] = hide[x];
