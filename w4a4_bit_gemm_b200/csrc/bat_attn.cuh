@@ -172,12 +172,14 @@ struct AttnDeal {
   __device__ __forceinline__ int64_t start(int i) const { return per * i + rem * static_cast<uint32_t>(i) / ctas; }
 };
 
-// The chunks of all sequences, and the place of the first chunk of CTA i's run (one warp,
-// together; every lane gets it).
+// The chunks of all sequences, and the place of the first chunk of CTA i's run, with its sequence
+// (one warp, together; every lane gets them).
 template <int kTile>
-__device__ __forceinline__ AttnMark attn_mark(const AttnParams& p, int cta, int lane, int64_t& run) {
+__device__ __forceinline__ AttnMark attn_mark(const AttnParams& p, int cta, int lane, int64_t& run, AttnSeq& seq) {
   AttnMark mk;
-  const int64_t w0 = lane < p.B ? attn_seq_chunks<kTile>(p, attn_seq(p, lane)) : 0;
+  seq = AttnSeq{0, 0, 0};
+  if (lane < p.B) seq = attn_seq(p, lane);
+  const int64_t w0 = lane < p.B ? attn_seq_chunks<kTile>(p, seq) : 0;
   int64_t total = w0;
   for (int b = lane + 32; b < p.B; b += 32) total += attn_seq_chunks<kTile>(p, attn_seq(p, b));
 #pragma unroll
@@ -204,11 +206,21 @@ __device__ __forceinline__ AttnMark attn_mark(const AttnParams& p, int cta, int 
     }
     x -= all;
   }
-  const AttnSeq s = attn_seq(p, pl.b);
-  const int nt = attn_tiles<kTile>(p, s);
+  if (pl.b < 32) {
+    seq.t0 = __shfl_sync(0xffffffffu, seq.t0, pl.b);
+    seq.n = __shfl_sync(0xffffffffu, seq.n, pl.b);
+    seq.len = __shfl_sync(0xffffffffu, seq.len, pl.b);
+  } else {
+    seq = attn_seq(p, pl.b);
+  }
+  const int nt = attn_tiles<kTile>(p, seq);
   for (int t0 = 0; t0 < nt; t0 += 32) {
     const int t = t0 + lane;
-    const int c = t < nt ? attn_chunks<kTile>(p, s, t) : 0;
+    const int c = t < nt ? attn_chunks<kTile>(p, seq, t) : 0;
+    if (nt == 1) {  // (the usual decode step)
+      pl.chunks = __shfl_sync(0xffffffffu, c, 0);
+      break;
+    }
     const int64_t w = static_cast<int64_t>(c) * p.head_units;
     const int64_t inc = attn_warp_scan(w, lane);
     const int64_t all = __shfl_sync(0xffffffffu, inc, 31);
@@ -372,12 +384,15 @@ __host__ __device__ constexpr int attn_factor_floats(int nb, int ls) {
   return (na + 3) / 4 * 4 + nbf <= kv::kFacFloats ? (na + 3) / 4 * 4 + (nbf + 3) / 4 * 4 : 0;
 }
 // (no barrier: the caller's next one orders it)
-__device__ __forceinline__ AttnFactors attn_stage_factors(float* dst, const float* a, const float* b, int nb, int ls) {
+// Threads from `tid` 0 up, `nt` of them, take part (a negative tid does not).
+__device__ __forceinline__ AttnFactors attn_stage_factors(float* dst, const float* a, const float* b, int nb, int ls,
+                                                          int tid, int nt) {
   if (attn_factor_floats(nb, ls) == 0) return AttnFactors{a, b, ls};
   const int na = 1 << (2 * ls), nbf = nb << (10 - 2 * ls);
   float* db = dst + (na + 3) / 4 * 4;
-  for (int i = threadIdx.x; i < na; i += blockDim.x) dst[i] = __ldg(a + i);
-  for (int i = threadIdx.x; i < nbf; i += blockDim.x) db[i] = __ldg(b + i);
+  if (tid < 0) return AttnFactors{dst, db, ls};
+  for (int i = tid; i < na; i += nt) dst[i] = __ldg(a + i);
+  for (int i = tid; i < nbf; i += nt) db[i] = __ldg(b + i);
   return AttnFactors{dst, db, ls};
 }
 // The four outputs n = q, 8 + q, 16 + q, 24 + q (q < 8) of block `blk`: y = x (B_blk (x) A), x the
@@ -472,6 +487,7 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
   float* fac_q = reinterpret_cast<float*>(sq + kR * kDP);
   float* fac_o = fac_q + (p.qa ? attn_factor_floats(p.nb, p.qls) : 0);
   __shared__ AttnPlace s_place;
+  __shared__ AttnSeq s_seq;
   __shared__ int64_t s_run;
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -479,21 +495,24 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
   allow_dependents();
   if (warp == 0) {
     int64_t run;
-    const AttnMark mk = attn_mark<0>(p, blockIdx.x, lane, run);
+    AttnSeq seq0;
+    const AttnMark mk = attn_mark<0>(p, blockIdx.x, lane, run, seq0);
     if (lane == 0) {
       s_place = mk.place;
+      s_seq = seq0;
       s_run = run;
       p.marks[blockIdx.x] = mk;
     }
   }
+  // the other warps bring the factors in meanwhile
   AttnFactors fq{nullptr, nullptr, 3}, fo{nullptr, nullptr, 3};
-  if (p.qa) fq = attn_stage_factors(fac_q, p.qa, p.qb, p.nb, p.qls);
-  if (p.oa) fo = attn_stage_factors(fac_o, p.oa, p.ob, p.nb, p.ols);
+  if (p.qa) fq = attn_stage_factors(fac_q, p.qa, p.qb, p.nb, p.qls, static_cast<int>(threadIdx.x) - 32, attn::kThreads - 32);
+  if (p.oa) fo = attn_stage_factors(fac_o, p.oa, p.ob, p.nb, p.ols, static_cast<int>(threadIdx.x) - 32, attn::kThreads - 32);
   __syncthreads();
   AttnPlace pl = s_place;
   int64_t left = s_run;
   if (left <= 0) return;
-  AttnSeq seq = attn_seq(p, pl.b);
+  AttnSeq seq = s_seq;
   const int hgs = p.head_units / p.Hkv;  // groups of kR heads of a KV head
   const int row_bytes = kFp8 ? p.D : p.D / 2;
   uint8_t* ring = reinterpret_cast<uint8_t*>(smem) + warp * C::kWarpBytes;
@@ -513,15 +532,15 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
 
     // ---- the warp's stream: a lane a token of its tiles
     int page_ahead = 0, off_ahead = -1;
-    auto look = [&](int chunk) {
+    auto look = [&](int chunk, int& page, int& off) {
       const int i = chunk * attn::kChunk + 32 * warp + lane;
-      off_ahead = -1;
+      off = -1;
       if (chunk >= last || i >= nv) return;
       const int j = span.token(i), pg = attn_page_of(p, j);
-      page_ahead = __ldg(pages + pg);
-      off_ahead = j - pg * p.page_size;
+      page = __ldg(pages + pg);
+      off = j - pg * p.page_size;
     };
-    auto found = [&]() -> int { return off_ahead >= 0 ? attn_row_at(p, page_ahead, off_ahead, h) : -1; };
+    auto found = [&](int page, int off) -> int { return off >= 0 ? attn_row_at(p, page, off, h) : -1; };
     // two lanes copy 32 bytes of a token each time
     auto copy = [&](int row, int st) {
       const uint32_t kd = ring32 + st * C::kStageBytes + (lane >> 1) * C::kKs + (lane & 1) * 16;
@@ -616,15 +635,21 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     };
 
     int rw[kS + 1];  // cache rows of tiles i .. i + kS - 1 of the warp, a token a lane
+    {
+      // the table's entries of all first tiles and the q rows are on their way together
+      int page[kS], off[kS];
 #pragma unroll
-    for (int k = 0; k < kS; ++k) {
-      look(first + k);
-      rw[k] = found();
+      for (int k = 0; k < kS; ++k) look(first + k, page[k], off[k]);
+      look(first + kS, page_ahead, off_ahead);
+      const int q_lines = (nrows * p.D * 2 + 127) / 128;
+      if (static_cast<int>(threadIdx.x) < q_lines)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q + tok * p.q_stride + static_cast<int64_t>(head0) * p.D + 64 * threadIdx.x));
+#pragma unroll
+      for (int k = 0; k < kS; ++k) rw[k] = found(page[k], off[k]);
     }
     load_scales(rw[0]);
 #pragma unroll
     for (int k = 0; k < kS; ++k) copy(rw[k], k);
-    look(first + kS);
 
     // ---- q rows (times P_q) in fp32, then in f16 with the row's power of two
     for (int i = threadIdx.x; i < kR * kNB * 8; i += attn::kThreads) {
@@ -699,8 +724,8 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     int st = 0;
     for (int ch = first; ch < last; ++ch) {
       const int par = (ch - first) & 1;
-      rw[kS] = found();
-      look(ch + kS + 1);
+      rw[kS] = found(page_ahead, off_ahead);
+      look(ch + kS + 1, page_ahead, off_ahead);
       put_scales(par ^ 1);
       load_scales(rw[2]);
       attn_copy_wait<kS - 1>();
@@ -956,7 +981,7 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
   const int i1 = blockIdx.x + 1;
   float* so = smem + warp * 260;  // [D] of this warp's row, its maximum and sum
   AttnFactors fo{nullptr, nullptr, 3};
-  if (p.oa) fo = attn_stage_factors(smem + 8 * 260, p.oa, p.ob, p.nb, p.ols);
+  if (p.oa) fo = attn_stage_factors(smem + 8 * 260, p.oa, p.ob, p.nb, p.ols, threadIdx.x, blockDim.x);
   __syncthreads();
   grid_dependency_wait();
   const AttnMark mk = p.marks[i1];

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(256) bat_attn_q_rows_kernel(const AttnQRowsPar
   allow_dependents();
   AttnFactors f{nullptr, nullptr, 3};
   if (p.a) {
-    f = attn_stage_factors(smem + 8 * 256, p.a, p.b, p.nb, p.ls);
+    f = attn_stage_factors(smem + 8 * 256, p.a, p.b, p.nb, p.ls, threadIdx.x, blockDim.x);
     __syncthreads();
   }
   const int64_t rows = p.T * p.Hq, step = static_cast<int64_t>(gridDim.x) * 8;
@@ -299,7 +299,8 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
   }
   if (warp == 15) {
     int64_t n;
-    const AttnMark mk = attn_mark<kTile>(p, blockIdx.x, lane, n);
+    AttnSeq seq0;
+    const AttnMark mk = attn_mark<kTile>(p, blockIdx.x, lane, n, seq0);
     if (lane == 0) {
       s_place = mk.place;
       s_run = n;
