@@ -148,6 +148,12 @@ def _need(t: torch.Tensor, dtype: torch.dtype, name: str, shape=None, device=Non
     return t
 
 
+def _plain(t, dtype: torch.dtype, index: int) -> bool:
+    """A contiguous tensor of `dtype` on device `index` (the quick form of _need's tests)."""
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.is_contiguous())
+
+
 def _need_bytes(t: torch.Tensor, name: str, nbytes: int, device) -> torch.Tensor:
     """A caller-supplied byte buffer the kernels write or read: large enough for its shape."""
     _need(t, torch.uint8, name, device=device)
@@ -604,7 +610,7 @@ def _attention_bytes(T, Hq, H, D, max_q_len) -> int:
     return bat_kv_attention_workspace_bytes(T, Hq, H, D, max_q_len)
 
 
-def _scratch(n: int, dev, stream, dtype=torch.uint8) -> torch.Tensor:
+def _scratch(n, dev, stream, dtype=torch.uint8) -> torch.Tensor:
     """A buffer of this call, in the allocator's order on the stream that uses it."""
     if stream is None:
         return torch.empty(n, dtype=dtype, device=dev)
@@ -640,14 +646,27 @@ def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q
     H = kcache.H
     if kcache.D != D or vcache.D != D or H != vcache.H or kcache.num_slots != vcache.num_slots:
         raise ValueError("the caches' shapes do not match each other and q")
-    kcache.check(dev)
-    vcache.check(dev)
-    _need(page_table, torch.int32, "page_table", None, dev)
+    # the usual case by a few quick tests (a small call's time is its checks); what fails one
+    # goes through the tests that say what is wrong
+    di, i32, u8 = q.get_device(), torch.int32, torch.uint8
+    n = kcache.num_slots * H * D
+    nc = n if kcache.fmt == "mxfp8" else n // 2
+    if not (kcache.fmt in _KV_FMT and vcache.fmt in _KV_FMT and kcache.fmt == vcache.fmt
+            and _plain(kcache.codes, u8, di) and _plain(vcache.codes, u8, di)
+            and _plain(kcache.scales, u8, di) and _plain(vcache.scales, u8, di)
+            and kcache.codes.numel() >= nc and vcache.codes.numel() >= nc
+            and kcache.scales.numel() >= n // 32 and vcache.scales.numel() >= n // 32):
+        kcache.check(dev)
+        vcache.check(dev)
+    if not _plain(page_table, i32, di):
+        _need(page_table, i32, "page_table", None, dev)
     if page_table.dim() != 2:
         raise ValueError("page_table must be two-dimensional")
     B, max_pages = page_table.shape
-    _need(kv_lens, torch.int32, "kv_lens", (B,), dev)
-    _need(q_starts, torch.int32, "q_starts", (B + 1,), dev)
+    if not (_plain(kv_lens, i32, di) and _plain(q_starts, i32, di) and kv_lens.dim() == 1
+            and q_starts.dim() == 1 and kv_lens.numel() == B and q_starts.numel() == B + 1):
+        _need(kv_lens, i32, "kv_lens", (B,), dev)
+        _need(q_starts, i32, "q_starts", (B + 1,), dev)
     Aq = Bq = Ao = Bo = None
     sq = so = 8
     if q_factors is not None:
@@ -664,7 +683,7 @@ def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q
     else:
         _need(workspace, torch.uint8, "workspace", None, dev)
     if out is None:
-        out = _scratch(T * Hq * D, dev, stream, torch.bfloat16).view(T, Hq, D)
+        out = _scratch((T, Hq, D), dev, stream, torch.bfloat16)
     else:
         _need(out, torch.bfloat16, "out", (T, Hq, D), dev)
     _check(lib().bat_kv_attention(
@@ -695,13 +714,21 @@ def bat_rmsnorm_quantize(X, weight, A=None, B=None, g_lo=None, g_hi=None,
     dev = X.device
     if fmt not in _KV_FMT:
         raise ValueError(f"unknown format {fmt!r}")
-    _need(weight, torch.bfloat16, "weight", (K,), dev)
+    # the usual case by a few quick tests, as in bat_kv_attention
+    di, bf, f32 = X.get_device(), torch.bfloat16, torch.float32
+    if not (_plain(weight, bf, di) and weight.dim() == 1 and weight.numel() == K):
+        _need(weight, bf, "weight", (K,), dev)
+    s = 8
     if (A is None) != (B is None):
         raise ValueError("A and B must both be given or both be None")
-    s = 8 if A is None else _gpk_factors(A, B, K, dev)
-    _clip_args(g_lo, g_hi, K // 32, dev)
-    if residual is not None:
-        _need(residual, torch.bfloat16, "residual", (M, K), dev)
+    if A is not None and not (_plain(A, f32, di) and _plain(B, f32, di) and A.shape == (8, 8)
+                              and B.shape == (K // 32, 4, 4)):
+        s = _gpk_factors(A, B, K, dev)
+    if not (_plain(g_lo, f32, di) and _plain(g_hi, f32, di) and g_lo.dim() == g_hi.dim() == 1
+            and g_lo.numel() == g_hi.numel() == K // 32):
+        _clip_args(g_lo, g_hi, K // 32, dev)
+    if residual is not None and not (_plain(residual, bf, di) and residual.shape == X.shape):
+        _need(residual, bf, "residual", (M, K), dev)
     _on_device(dev, stream)
     cls = MXFP8 if fmt == "mxfp8" else MXFP4
     if Xq is None:
@@ -718,7 +745,7 @@ def bat_rmsnorm_quantize(X, weight, A=None, B=None, g_lo=None, g_hi=None,
     if residual_out is not None:
         _need(residual_out, torch.bfloat16, "residual_out", (M, K), dev)
     elif residual is not None:
-        residual_out = _scratch(M * K, dev, stream, torch.bfloat16).view(M, K)
+        residual_out = _scratch((M, K), dev, stream, torch.bfloat16)
     if y_out is not None:
         _need(y_out, torch.float32, "y_out", (M, K), dev)
     st = Xq.struct()
