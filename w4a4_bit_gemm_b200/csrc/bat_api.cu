@@ -748,11 +748,12 @@ template <int kTile>
 bat_status_t launch_attn_join(const bat::AttnParams& p, int dev, int bit, cudaStream_t s) {
   if (p.ctas < 2) return BAT_OK;
   auto k = bat::bat_attn_join_kernel<kTile>;
-  const size_t max_smem = (8 * 260 + bat::kv::kFacFloats) * 4;
-  const size_t smem = (8 * 260 + (p.oa ? bat::attn_factor_floats(p.nb, p.ols) : 0)) * 4;
+  constexpr int kR = 8 * bat::AttnJoin<kTile>::kRows;  // rows a CTA at a time
+  const size_t max_smem = (kR * 260 + bat::kv::kFacFloats) * 4;
+  const size_t smem = ((p.oa ? kR * 260 : 0) + (p.oa ? bat::attn_factor_floats(p.nb, p.ols) : 0)) * 4;
   bat_status_t st = attn_smem(k, dev, bit, max_smem);
   if (st != BAT_OK) return st;
-  return launch_dependent(k, dim3(p.ctas - 1, p.unit_rows / 8), dim3(256), smem, s, p);
+  return launch_dependent(k, dim3(p.ctas - 1, (p.unit_rows + kR - 1) / kR), dim3(256), smem, s, p);
 }
 
 template <bool kFp8, int kDP>
@@ -779,9 +780,10 @@ bat_status_t launch_attn_tile(bat::AttnParams& p, uint16_t* qt, int dev, int sms
   q.ls = p.qls;
   q.sign = p.q_sign;
   q.scale_log2 = p.scale_log2;
-  const int64_t want = (p.T * p.Hq + 7) / 8, cap = static_cast<int64_t>(sms) * 8;
-  const size_t q_smem = (8 * 256 + (p.qa ? bat::attn_factor_floats(p.nb, p.qls) : 0)) * 4;
-  bat::bat_attn_q_rows_kernel<<<static_cast<unsigned>(want < cap ? want : cap), 256, q_smem, s>>>(q);
+  constexpr int kL = kDP / 8;  // lanes a row
+  const int64_t want = (p.T * p.Hq * kL + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
+  const size_t q_smem = (8 * (32 / kL) * (8 * kL + 4) + (p.qa ? bat::attn_factor_floats(p.nb, p.qls) : 0)) * 4;
+  bat::bat_attn_q_rows_kernel<kL><<<static_cast<unsigned>(want < cap ? want : cap), 256, q_smem, s>>>(q);
   st = cuda_status(cudaGetLastError());
   if (st != BAT_OK) return st;
   st = launch_dependent(k, dim3(p.ctas), dim3(bat::attn_tile::kThreads), C::kSmem, s, p, qmap);

@@ -972,16 +972,23 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
 
 // ---------------------------------------------------------------- joining partial results
 // CTA (x, y): if CTA x + 1's run begins inside a unit, and no earlier run does, the parts
-// of that unit (the last of CTA x, then the first of x + 1, x + 2, ...) are joined here, a warp a
-// row. kTile as in the kernel that wrote them. Bound: the parts' bytes, or launch latency.
+// of that unit (the last of CTA x, then the first of x + 1, x + 2, ...) are joined here, a warp a row
+// for the row kernel's units, four rows a warp at a time for the tile kernel's (their parts on
+// their way together). kTile as in the kernel that wrote them. Bound:
+// the parts' bytes from L2, or latency.
+template <int kTile>
+struct AttnJoin {
+  static constexpr int kRows = kTile ? 4 : 1;
+};
 template <int kTile>
 __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) {
   extern __shared__ __align__(16) float smem[];
+  constexpr int kR = AttnJoin<kTile>::kRows;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i1 = blockIdx.x + 1;
-  float* so = smem + warp * 260;  // [D] of this warp's row, its maximum and sum
+  float* so = smem + warp * (kR * 260);  // [kR][260]: this warp's rows, when P_o is applied
   AttnFactors fo{nullptr, nullptr, 3};
-  if (p.oa) fo = attn_stage_factors(smem + 8 * 260, p.oa, p.ob, p.nb, p.ols, threadIdx.x, blockDim.x);
+  if (p.oa) fo = attn_stage_factors(smem + 8 * kR * 260, p.oa, p.ob, p.nb, p.ols, threadIdx.x, blockDim.x);
   __syncthreads();
   grid_dependency_wait();
   const AttnMark mk = p.marks[i1];
@@ -997,76 +1004,98 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
   const AttnSeq seq = attn_seq(p, pl.b);
   const int hgs = p.head_units / p.Hkv;
   const int h = pl.hu / hgs, hg = pl.hu - h * hgs;
-  for (int rr = blockIdx.y * 8 + warp; rr < rows; rr += gridDim.y * 8) {
-    int64_t tok;
-    int head;
-    if (kTile) {
-      const int64_t row = static_cast<int64_t>(pl.tile) * kTile + rr;
-      const int64_t t = row / p.G;
-      if (t >= seq.n) break;
-      tok = seq.t0 + t;
-      head = h * p.G + static_cast<int>(row - t * p.G);
-    } else {
-      if (hg * rows + rr >= p.G) break;
-      tok = seq.t0 + pl.tile;
-      head = h * p.G + hg * rows + rr;
-    }
+  // rows of the unit that are there
+  const int64_t there = kTile ? static_cast<int64_t>(seq.n) * p.G - static_cast<int64_t>(pl.tile) * kTile
+                              : p.G - hg * rows;
+  const int nrows = static_cast<int>(there < rows ? there : rows);
+  const int quads = p.D >> 2;  // float4 a row: this lane's are lane and lane + 32
+  for (int r0 = (blockIdx.y * 8 + warp) * kR; r0 < nrows; r0 += gridDim.y * 8 * kR) {
     // running over the parts in order: maximum, sum and o, as in the kernels
-    float mm = -INFINITY, sum = 0.0f;
-    float2 acc[4];
+    float mm[kR], sum[kR];
+    float4 acc[kR][2];
+    bool bad[kR];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] = make_float2(0.0f, 0.0f);
-    bool bad = false;
+    for (int k = 0; k < kR; ++k) {
+      mm[k] = -INFINITY;
+      sum[k] = 0.0f;
+      bad[k] = false;
+      acc[k][0] = acc[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+#pragma unroll kR == 1 ? 4 : 1
     for (int i = i1 - 1; i < end; ++i) {
       const int64_t xi = deal.start(i);
       if (xi >= deal.start(i + 1)) continue;  // an empty run
       // the unit is the first of CTA i's run if the run begins inside the unit (or at it)
-      const int64_t at = (2 * static_cast<int64_t>(i) + (xi >= u0 ? 0 : 1)) * rows + rr;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-      float2 v[4];
+      const int64_t at = (2 * static_cast<int64_t>(i) + (xi >= u0 ? 0 : 1)) * rows;
+      float2 ml[kR];
+      float4 v[kR][2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (64 * k + 2 * lane < p.D) v[k] = *reinterpret_cast<const float2*>(p.part_o + at * p.D + 64 * k + 2 * lane);
-      bad |= ml.y != ml.y;
-      if (ml.x == -INFINITY) continue;  // saw nothing
-      const float mn = fmaxf(mm, ml.x);
-      const float fo = attn_exp2(mm - mn), fi = attn_exp2(ml.x - mn);
-      mm = mn;
-      sum = sum * fo + ml.y * fi;
+      for (int k = 0; k < kR; ++k) {
+        const int64_t row = at + min(r0 + k, nrows - 1);
+        ml[k] = *reinterpret_cast<const float2*>(p.part_ml + 2 * row);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (64 * k + 2 * lane < p.D) {
-          acc[k].x = acc[k].x * fo + v[k].x * fi;
-          acc[k].y = acc[k].y * fo + v[k].y * fi;
-        }
-    }
-    if (bad) sum = NAN;
-    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-    uint16_t* dst = p.out + (tok * p.Hq + head) * p.D;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int d = 64 * k + 2 * lane;
-      acc[k].x *= inv;
-      acc[k].y *= inv;
-      if (d >= p.D) break;
-      if (p.oa != nullptr)
-        *reinterpret_cast<float2*>(so + d) = acc[k];
-      else
-        *reinterpret_cast<uint32_t*>(dst + d) = attn_pack(acc[k].x, acc[k].y);
-    }
-    if (p.oa != nullptr) {
-      __syncwarp();
-      for (int i = lane; i < p.nb * 8; i += 32) {
-        float y[4];
-        attn_block_apply(fo, i >> 3, so + 32 * (i >> 3), i & 7, y);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          dst[32 * (i >> 3) + 8 * j + (i & 7)] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
+        for (int g = 0; g < 2; ++g)
+          if (lane + 32 * g < quads) v[k][g] = *(reinterpret_cast<const float4*>(p.part_o + row * p.D) + lane + 32 * g);
       }
-      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < kR; ++k) {
+        bad[k] |= ml[k].y != ml[k].y;
+        if (ml[k].x == -INFINITY) continue;  // saw nothing
+        const float mn = fmaxf(mm[k], ml[k].x);
+        const float f0 = attn_exp2(mm[k] - mn), f1 = attn_exp2(ml[k].x - mn);
+        mm[k] = mn;
+        sum[k] = sum[k] * f0 + ml[k].y * f1;
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          if (lane + 32 * g < quads) {
+            acc[k][g].x = acc[k][g].x * f0 + v[k][g].x * f1;
+            acc[k][g].y = acc[k][g].y * f0 + v[k][g].y * f1;
+            acc[k][g].z = acc[k][g].z * f0 + v[k][g].z * f1;
+            acc[k][g].w = acc[k][g].w * f0 + v[k][g].w * f1;
+          }
+      }
     }
-    if (p.lse && lane == 0)
-      p.lse[tok * p.Hq + head] = sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * 0.69314718055994531f;
+#pragma unroll
+    for (int k = 0; k < kR; ++k) {
+      if (r0 + k >= nrows) break;
+      int64_t tok;
+      int head;
+      if (kTile) {
+        const int64_t row = static_cast<int64_t>(pl.tile) * kTile + r0 + k;
+        const int64_t t = row / p.G;
+        tok = seq.t0 + t;
+        head = h * p.G + static_cast<int>(row - t * p.G);
+      } else {
+        tok = seq.t0 + pl.tile;
+        head = h * p.G + hg * rows + r0 + k;
+      }
+      const float l = bad[k] ? NAN : sum[k];
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      uint16_t* dst = p.out + (tok * p.Hq + head) * p.D;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int q = lane + 32 * g;
+        if (q >= quads) break;
+        const float4 y = make_float4(acc[k][g].x * inv, acc[k][g].y * inv, acc[k][g].z * inv, acc[k][g].w * inv);
+        if (p.oa != nullptr)
+          *reinterpret_cast<float4*>(so + k * 260 + 4 * q) = y;
+        else
+          *reinterpret_cast<uint2*>(dst + 4 * q) = make_uint2(attn_pack(y.x, y.y), attn_pack(y.z, y.w));
+      }
+      if (p.oa != nullptr) {
+        __syncwarp();
+        for (int i = lane; i < p.nb * 8; i += 32) {
+          float y[4];
+          attn_block_apply(fo, i >> 3, so + k * 260 + 32 * (i >> 3), i & 7, y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dst[32 * (i >> 3) + 8 * j + (i & 7)] = __bfloat16_as_ushort(__float2bfloat16_rn(y[j]));
+        }
+        __syncwarp();
+      }
+      if (p.lse && lane == 0)
+        p.lse[tok * p.Hq + head] = l == 0.0f ? -INFINITY : (mm[k] + log2f(l)) * 0.69314718055994531f;
+    }
   }
 }
 

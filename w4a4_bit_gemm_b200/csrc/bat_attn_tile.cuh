@@ -130,7 +130,8 @@ __host__ __device__ constexpr int attn_v_order(int i) {
 }
 
 // Rows of q (P_q) in f16, times the power of two that brings the row's largest channel to
-// [2^14, 2^15), and the factor that takes it back; warp a row.
+// [2^14, 2^15), and the factor that takes it back. kL lanes a row, 8 channels each; a warp has
+// four steps' rows on their way at once (bound: HBM, 4 bytes an element).
 struct AttnQRowsParams {
   const uint16_t* q;
   int64_t q_stride;
@@ -142,61 +143,81 @@ struct AttnQRowsParams {
   int Hq, G, D, nb, ls;
   float sign, scale_log2;
 };
+template <int kL>
 __global__ void __launch_bounds__(256) bat_attn_q_rows_kernel(const AttnQRowsParams p) {
   extern __shared__ __align__(16) float smem[];
+  constexpr int kRows = 32 / kL, kAhead = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* sx = smem + warp * 256;  // the row in fp32
+  const int v = lane % kL, sub = lane / kL;
+  float* sx = smem + (warp * kRows + sub) * (8 * kL + 4);  // the row in fp32
   allow_dependents();
   AttnFactors f{nullptr, nullptr, 3};
   if (p.a) {
-    f = attn_stage_factors(smem + 8 * 256, p.a, p.b, p.nb, p.ls, threadIdx.x, blockDim.x);
+    f = attn_stage_factors(smem + 8 * kRows * (8 * kL + 4), p.a, p.b, p.nb, p.ls, threadIdx.x, blockDim.x);
     __syncthreads();
   }
-  const int64_t rows = p.T * p.Hq, step = static_cast<int64_t>(gridDim.x) * 8;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + warp; row < rows; row += step) {
-    const int64_t t = row / p.Hq;
-    const int hq = static_cast<int>(row - t * p.Hq), h = hq / p.G;
-    const int64_t dst = (h * p.T + t) * p.G + (hq - h * p.G);
-    const bool has = 8 * lane < p.D;  // 8 channels a lane
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (has) w = *(reinterpret_cast<const uint4*>(p.q + t * p.q_stride + static_cast<int64_t>(hq) * p.D) + lane);
-    float x[8] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y), bf16lo(w.z), bf16hi(w.z), bf16lo(w.w), bf16hi(w.w)};
-    if (p.a) {
-      if (has) {
-        reinterpret_cast<float4*>(sx)[2 * lane] = make_float4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<float4*>(sx)[2 * lane + 1] = make_float4(x[4], x[5], x[6], x[7]);
-      }
-      __syncwarp();
-      float y[2][4];
+  const bool in = 8 * v < p.D;
+  const uint32_t hq_n = p.Hq;
+  const uint32_t rows = static_cast<uint32_t>(p.T) * hq_n;  // at most 2^30
+  const uint32_t step = gridDim.x * 8 * kRows;
+  for (uint32_t r0 = (blockIdx.x * 8 + warp) * kRows; r0 < rows; r0 += kAhead * step) {
+    uint4 w[kAhead];
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (32 * g + lane < 8 * p.nb) attn_block_apply(f, (32 * g + lane) >> 3, sx + 32 * ((32 * g + lane) >> 3), lane & 7, y[g]);
-      __syncwarp();
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t row = r0 + k * step + sub;
+      const uint32_t t = row / hq_n;
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows && in)
+        w[k] = __ldg(reinterpret_cast<const uint4*>(p.q + t * p.q_stride + static_cast<int64_t>(row - t * hq_n) * p.D) + v);
+    }
 #pragma unroll
-      for (int g = 0; g < 2; ++g)
-        if (32 * g + lane < 8 * p.nb)
+    for (int k = 0; k < kAhead; ++k) {
+      const uint32_t row = r0 + k * step + sub;
+      if (r0 + k * step >= rows) break;
+      float x[8] = {bf16lo(w[k].x), bf16hi(w[k].x), bf16lo(w[k].y), bf16hi(w[k].y),
+                    bf16lo(w[k].z), bf16hi(w[k].z), bf16lo(w[k].w), bf16hi(w[k].w)};
+      if (p.a) {
+        *reinterpret_cast<float4*>(sx + 8 * v) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(sx + 8 * v + 4) = make_float4(x[4], x[5], x[6], x[7]);
+        __syncwarp();
+        // lane v takes outputs v % 8 and that + 8, + 16, + 24 of blocks v / 8 and kL / 8 more
+        constexpr int kPer = kL >= 8 ? 2 : 4;  // 2 kL such items a row
+        float y[kPer][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) sx[32 * ((32 * g + lane) >> 3) + 8 * j + (lane & 7)] = y[g][j];
-      __syncwarp();
-      if (has) {
-        const float4 a = reinterpret_cast<const float4*>(sx)[2 * lane], b = reinterpret_cast<const float4*>(sx)[2 * lane + 1];
+        for (int g = 0; g < kPer; ++g) {
+          const int item = v + g * kL;
+          if (item < 8 * p.nb) attn_block_apply(f, item >> 3, sx + 32 * (item >> 3), item & 7, y[g]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int g = 0; g < kPer; ++g) {
+          const int item = v + g * kL;
+          if (item < 8 * p.nb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sx[32 * (item >> 3) + 8 * j + (item & 7)] = y[g][j];
+        }
+        __syncwarp();
+        const float4 a = *reinterpret_cast<const float4*>(sx + 8 * v), b = *reinterpret_cast<const float4*>(sx + 8 * v + 4);
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
         x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        __syncwarp();
       }
-      __syncwarp();
+      float mx = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mx = in ? fmaxf(mx, fabsf(x[j])) : 0.0f;
+#pragma unroll
+      for (int d = kL / 2; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+      float down;
+      const float up = attn_row_up(mx, down) * p.sign;
+      if (row >= rows) continue;
+      const uint32_t t = row / hq_n, hq = row - t * hq_n, h = hq / p.G;
+      const int64_t dst = (h * p.T + t) * p.G + (hq - h * p.G);
+      if (in)
+        *(reinterpret_cast<uint4*>(p.out + dst * p.D) + v) =
+            make_uint4(attn_pack_f16(x[0] * up, x[1] * up), attn_pack_f16(x[2] * up, x[3] * up),
+                       attn_pack_f16(x[4] * up, x[5] * up), attn_pack_f16(x[6] * up, x[7] * up));
+      if (v == 0) p.fac[dst] = down * p.scale_log2;
     }
-    float mx = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mx = fmaxf(mx, fabsf(x[j]));
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    float down;
-    const float up = attn_row_up(mx, down) * p.sign;
-    if (has)
-      *(reinterpret_cast<uint4*>(p.out + dst * p.D) + lane) =
-          make_uint4(attn_pack_f16(x[0] * up, x[1] * up), attn_pack_f16(x[2] * up, x[3] * up),
-                     attn_pack_f16(x[4] * up, x[5] * up), attn_pack_f16(x[6] * up, x[7] * up));
-    if (lane == 0) p.fac[dst] = down * p.scale_log2;
   }
 }
 
