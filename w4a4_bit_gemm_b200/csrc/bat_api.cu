@@ -705,6 +705,8 @@ bat_status_t attn_smem(Kernel k, int dev, int bit, size_t max_bytes) {
   return BAT_OK;
 }
 
+// A launch that may overlap the end of the kernel before it (programmatic stream
+// serialization): the kernel waits (grid_dependency_wait) before it reads what others write.
 template <class Kernel, class... Args>
 bat_status_t launch_dependent(Kernel k, dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
   cudaLaunchConfig_t cfg = {};
@@ -740,8 +742,7 @@ bat_status_t launch_attn_rows(bat::AttnParams& p, int dev, int sms, int bit, cud
   int per_sm = bat::attn_rows_per_sm(kFp8, kNB, kNT);
   while (per_sm > 1 && per_sm * (smem + 2048) > 227 * 1024) --per_sm;
   p.ctas = per_sm * sms < kAttnRowCtas ? per_sm * sms : kAttnRowCtas;
-  k<<<p.ctas, bat::attn::kThreads, smem, s>>>(p);
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(k, dim3(p.ctas), dim3(bat::attn::kThreads), smem, s, p);
 }
 
 template <int kTile>
@@ -783,8 +784,8 @@ bat_status_t launch_attn_tile(bat::AttnParams& p, uint16_t* qt, int dev, int sms
   constexpr int kL = kDP / 8;  // lanes a row
   const int64_t want = (p.T * p.Hq * kL + 255) / 256, cap = static_cast<int64_t>(sms) * 8;
   const size_t q_smem = (8 * (32 / kL) * (8 * kL + 4) + (p.qa ? bat::attn_factor_floats(p.nb, p.qls) : 0)) * 4;
-  bat::bat_attn_q_rows_kernel<kL><<<static_cast<unsigned>(want < cap ? want : cap), 256, q_smem, s>>>(q);
-  st = cuda_status(cudaGetLastError());
+  st = launch_dependent(bat::bat_attn_q_rows_kernel<kL>, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256),
+                        q_smem, s, q);
   if (st != BAT_OK) return st;
   st = launch_dependent(k, dim3(p.ctas), dim3(bat::attn_tile::kThreads), C::kSmem, s, p, qmap);
   if (st != BAT_OK) return st;
@@ -808,8 +809,7 @@ bat_status_t launch_norm(const bat::NormParams& p, int sms, cudaStream_t s) {
                                                    : bat::bat_rmsnorm_quantize_kernel<0, kX, kFp8, 512>;
   const int64_t cap = static_cast<int64_t>(sms) * (nt <= 256 ? 512 / nt : 1);
   const unsigned grid = static_cast<unsigned>(p.M < cap ? p.M : cap);
-  k<<<grid, nt, 0, s>>>(p);
-  return cuda_status(cudaGetLastError());
+  return launch_dependent(k, dim3(grid), dim3(nt), 0, s, p);
 }
 
 }  // namespace

@@ -492,6 +492,9 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane & 3, r = lane >> 2;
+  // everything below reads what kernels before this one write; the joining kernel may start its
+  // set-up once that is complete
+  grid_dependency_wait();
   allow_dependents();
   if (warp == 0) {
     int64_t run;
@@ -991,6 +994,7 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
   if (p.oa) fo = attn_stage_factors(smem + 8 * kR * 260, p.oa, p.ob, p.nb, p.ols, threadIdx.x, blockDim.x);
   __syncthreads();
   grid_dependency_wait();
+  allow_dependents();
   const AttnMark mk = p.marks[i1];
   const int64_t total = mk.total, x = mk.x;
   if (x >= total) return;

@@ -154,6 +154,9 @@ __global__ void __launch_bounds__(256) bat_attn_q_rows_kernel(const AttnQRowsPar
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int v = lane % kL, sub = lane / kL;
   float* sx = smem + (warp * kRows + sub) * (8 * kL + 4);  // the row in fp32
+  // (in this order: the tile kernel reads the cache and the lengths without a wait of its own, so it
+  // may not start before the kernels ahead of this one are complete)
+  grid_dependency_wait();
   allow_dependents();
   AttnFactors f{nullptr, nullptr, 3};
   if (p.a) {

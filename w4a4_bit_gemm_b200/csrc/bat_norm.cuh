@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
   __shared__ __align__(16) float sa[64];
   __shared__ float red[2][norm::kMaxThreads / 32];
   const int tid = threadIdx.x, nt = blockDim.x, nvec = p.K >> 4;
+  grid_dependency_wait();  // launched with programmatic serialization
+  allow_dependents();      // the GEMM after it waits for this kernel's end
   if (kX == 1 && tid < 64) sa[tid] = p.a[tid];
   constexpr int kN = kV > 0 ? kV : 1;
   float bq[kN][8], r_lo[kN], r_hi[kN];
