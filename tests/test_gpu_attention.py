@@ -49,11 +49,13 @@ def _apply(x, P):
 class Setup:
     """Caches filled through bat_kv_quantize (rows no sequence owns hold NaN), and the call."""
 
-    def __init__(self, bat, seqs, Hq, H, D, fmt, page, seed=0, q_pad=0, qf=None, of=None, extra_rows=0, kv_scale=1.0):
+    # capacity: tokens the page table has room for; with room for many, chunks go to the tile kernel
+    def __init__(self, bat, seqs, Hq, H, D, fmt, page, seed=0, q_pad=0, qf=None, of=None, extra_rows=0, kv_scale=1.0,
+                 capacity=1 << 20):
         g = torch.Generator().manual_seed(seed)
         self.bat, self.seqs, self.Hq, self.H, self.D, self.page = bat, seqs, Hq, H, D, page
         pages = [max(1, -(-L // page)) for _, L in seqs]
-        self.max_pages = max(pages)
+        self.max_pages = max(max(pages), capacity // page)
         pool = sum(pages) + 2
         perm = torch.randperm(pool, generator=g).tolist()
         table = torch.full((len(seqs), self.max_pages), 2 ** 30, dtype=torch.int32)  # unused entries: garbage
@@ -184,6 +186,16 @@ def test_attention_matches_formula(bat, case):
     torch.cuda.synchronize()
     s.check(out, lse, **kw)
     assert bat.bat_device_error() == 0
+
+
+@pytest.mark.parametrize("case", [3, 8, 14, 15, 16, 17, 18, 19, 20, 21, 22])
+def test_attention_chunks_on_the_row_kernel(bat, case):
+    """The same chunks where the call may expect single tokens, and with a table of the lengths' size."""
+    seqs, Hq, H, D, fmt, page, kw = CASES[case]
+    s = Setup(bat, seqs, Hq, H, D, fmt, page, seed=200 + case, qf=8, of=8, capacity=0)
+    lse = torch.empty(s.T, Hq, dtype=torch.float32, device="cuda")
+    s.check(s.call(max_q_len=1, lse=lse, **kw), None, **kw)
+    s.check(s.call(**kw), None, **kw)
 
 
 @pytest.mark.parametrize("case,qs,os", [(1, 8, None), (1, None, 8), (2, 4, 16), (3, 8, 8), (5, 1, 32), (7, 8, 8),
@@ -325,7 +337,7 @@ def test_attention_wrong_max_q_len_is_still_right(bat):
 
 def test_attention_clamps_lengths(bat):
     """A length past the table is clamped and reported; nothing outside is read."""
-    s = Setup(bat, [(1, 64)], 4, 2, 64, "mxfp8", 16, seed=15)
+    s = Setup(bat, [(1, 64)], 4, 2, 64, "mxfp8", 16, seed=15, capacity=0)
     ref = s.call()
     s.kv_lens.fill_(1000)
     out = s.call()

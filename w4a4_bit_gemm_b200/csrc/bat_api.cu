@@ -683,13 +683,19 @@ size_t attn_part_bytes(int64_t ctas, int64_t rows, int64_t D) {
                              round_up(ctas * static_cast<int64_t>(sizeof(bat::AttnMark)), 256));
 }
 
-// Query rows of a KV head (tokens x heads of the group) from which a chunk goes to the tile
-// kernel.
-constexpr int64_t kAttnTileRows = 64;
-constexpr int kAttnTileCtas = 160;
-bool attn_use_tile(int64_t G, int64_t max_q_len) {
-  return max_q_len > 1 && max_q_len >= (kAttnTileRows + G - 1) / G;
+// Which kernel. The row kernel reads the cache once for every new token, the tile kernel once for
+// 256 rows, but the latter's fixed time is longer and a tile costs the same for few rows. Measured
+// (B200, KV8, us, row / tile kernel): 32 / 8 heads of 128: 8 sequences x 16384 tokens: 2 new tokens
+// 149 / 209, 4: 262 / 209, 8: 501 / 211; 8 x 2000: 2: 39 / 52, 4: 55 / 52, 8: 90 / 53; 1 x 2000: 8:
+// 32 / 40, 16: 39 / 41, 32: 55 / 45. 28 / 4 heads of 64: 8 x 16384: 4: 93 / 106, 8: 157 / 107; 8 x 2000: 8:
+// 39 / 43, 16: 59 / 45. So: from 4 (6 for narrow heads) new tokens on, if the row kernel's reads, at
+// most new tokens x KV heads x cached tokens x channels as far as the host knows, are worth it.
+int64_t attn_tile_tokens(int64_t D) { return D > 64 ? 4 : 6; }
+bool attn_use_tile(int64_t T, int64_t H, int64_t D, int64_t capacity, int64_t max_q_len) {
+  return max_q_len >= attn_tile_tokens(D) &&
+         static_cast<double>(T * H) * static_cast<double>(capacity) * static_cast<double>(D) >= 48e6;
 }
+constexpr int kAttnTileCtas = 160;
 int64_t attn_tile_rows(int64_t D) { return D <= 128 ? 256 : 128; }
 
 template <class Kernel>
@@ -1123,9 +1129,11 @@ size_t bat_kv_attention_workspace_bytes(int64_t T, int64_t Hq, int64_t H, int64_
                                         int64_t max_q_len) {
   if (T < 1 || Hq < 1 || H < 1 || Hq % H != 0 || D < 32 || D % 32 != 0 || D > 256 || max_q_len < 1) return 0;
   if (T > kMaxRows / Hq) return 0;
-  if (!attn_use_tile(Hq / H, max_q_len)) return attn_part_bytes(kAttnRowCtas, attn_row_unit(Hq / H, D), D);
-  return attn_part_bytes(kAttnTileCtas, attn_tile_rows(D), D) +
-         static_cast<size_t>(round_up(T * Hq * D * 2, 256) + round_up(T * Hq * 4, 256));
+  const size_t row = attn_part_bytes(kAttnRowCtas, attn_row_unit(Hq / H, D), D);
+  if (max_q_len < attn_tile_tokens(D)) return row;
+  const size_t tile = attn_part_bytes(kAttnTileCtas, attn_tile_rows(D), D) +
+                      static_cast<size_t>(round_up(T * Hq * D * 2, 256) + round_up(T * Hq * 4, 256));
+  return row > tile ? row : tile;
 }
 
 bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_stride,
@@ -1208,7 +1216,7 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
   p.q_sign = scale < 0.0f ? -1.0f : 1.0f;
   const bool fp8 = K->fmt == BAT_KV_MXFP8;
-  const bool tile = attn_use_tile(p.G, max_q_len);
+  const bool tile = attn_use_tile(T, H, D, p.capacity, max_q_len);
   const int unit = tile ? static_cast<int>(attn_tile_rows(D)) : attn_row_unit(p.G, D);
   const int64_t ctas = tile ? kAttnTileCtas : kAttnRowCtas;
   p.unit_rows = unit;
