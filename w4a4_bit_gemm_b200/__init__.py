@@ -687,7 +687,7 @@ def bat_kv_attention(q, kcache: KVCache, vcache: KVCache, page_table, kv_lens, q
     else:
         _need(out, torch.bfloat16, "out", (T, Hq, D), dev)
     _check(lib().bat_kv_attention(
-        q.data_ptr(), T, Hq, s0 if T > 1 else max(s0, Hq * D), ctypes.byref(kcache.struct()),
+        q.data_ptr(), T, Hq, s0 if T > 1 else Hq * D, ctypes.byref(kcache.struct()),
         ctypes.byref(vcache.struct()), page_table.data_ptr(), B, max_pages, page_size,
         kv_lens.data_ptr(), q_starts.data_ptr(), max_q_len, D ** -0.5 if scale is None else scale, window,
         sinks, _ptr(Aq), sq, _ptr(Bq), _ptr(Ao), so, _ptr(Bo), out.data_ptr(), _ptr(lse),
