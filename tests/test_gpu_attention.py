@@ -353,3 +353,122 @@ def test_attention_batch_of_many_sequences(bat):
             for _ in range(77)]
     s = Setup(bat, seqs, 4, 2, 64, "mxfp8", 16, seed=16)
     s.check(s.call())
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("seqs", [[(1, 700)], [(40, 700)]])
+def test_attention_tokens_of_very_different_size(bat, fmt, seqs):
+    """Keys and values whose tokens differ by up to 2^24: the scales of a tile do not drown small ones."""
+    s = Setup(bat, seqs, 4, 2, 128, fmt, 16, seed=17)
+    g = torch.Generator().manual_seed(18)
+    eyeA, eyeB = torch.eye(8).cuda(), torch.eye(4).repeat(4, 1, 1).cuda()
+    L = seqs[0][1]
+    j = torch.arange(L)
+    slot = (s.table[0].cpu()[j // 16].long() * 16 + j % 16).cuda()
+    for c in range(2):
+        size = torch.exp2(torch.randint(-12, 13, (L, 1, 1), generator=g).float())
+        x = (torch.randn(L, 2, 128, generator=g) * size).bfloat16().cuda()
+        bat.bat_kv_quantize(x, eyeA, eyeB, slot, s.caches[c])
+        s.vals[c][0] = bat.bat_kv_dequantize(s.caches[c], slot).double()
+    for scale in (2.0 ** -14, 2.0 ** -8):
+        s.check(s.call(scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("seqs", [[(1, 300)], [(50, 300)]])
+def test_attention_scales_at_any_address(bat, seqs):
+    """Scale arrays that do not begin at a word."""
+    s = Setup(bat, seqs, 4, 2, 128, "mxfp8", 16, seed=19)
+    ref = s.call()
+    for c in s.caches:
+        wide = torch.zeros(c.scales.numel() + 8, dtype=torch.uint8, device="cuda")
+        wide[1:1 + c.scales.numel()] = c.scales
+        c.scales = wide[1:1 + c.scales.numel()]
+    assert torch.equal(s.call(), ref)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_attention_bad_q_stays_in_its_row(bat, value):
+    for seqs in ([(1, 300), (1, 20)], [(50, 300), (7, 20)]):
+        s = Setup(bat, seqs, 4, 2, 64, "mxfp8", 16, seed=20)
+        ref = s.call()
+        s.q[0, 1, 5] = value
+        out = s.call()
+        assert torch.isnan(out[0, 1]).all()
+        keep = torch.ones(s.T, 4, dtype=torch.bool, device="cuda")
+        keep[0, 1] = False
+        assert torch.equal(out[keep], ref[keep])
+
+
+def test_attention_many_chunks_batch(bat):
+    """More sequences than a warp scans at once, on the tile kernel, with a window."""
+    g = torch.Generator().manual_seed(5)
+    seqs = [(int(torch.randint(0, 40, (1,), generator=g)), int(torch.randint(1, 400, (1,), generator=g)))
+            for _ in range(50)]
+    for kw in ({}, {"window": 50, "sinks": 2}):
+        s = Setup(bat, seqs, 6, 2, 64, "mxfp4", 16, seed=21)
+        s.check(s.call(**kw), **kw)
+
+
+@pytest.mark.parametrize("kw", [{"window": 10 ** 9}, {"window": 10 ** 9, "sinks": 10 ** 9}, {"sinks": 5}, {"window": 3, "sinks": 10 ** 9}])
+def test_attention_windows_without_effect(bat, kw):
+    """Windows and sinks that hide nothing give the plain result's bits."""
+    for seqs in ([(1, 300), (1, 20)], [(90, 300), (7, 20)]):
+        s = Setup(bat, seqs, 4, 2, 64, "mxfp8", 16, seed=22)
+        ref, out = s.call(), s.call(**kw)
+        if kw.get("window") == 3:
+            s.check(out)  # every token is a sink: the same values, numbered another way
+        else:
+            assert torch.equal(out, ref)
+
+
+def test_attention_two_graphs_in_flight(bat):
+    """Two captured calls with workspaces of their own, replayed together on two streams."""
+    calls = []
+    for k, seqs in enumerate(([(1, 2500), (1, 40)], [(120, 2500)])):
+        s = Setup(bat, seqs, 8, 2, 128, "mxfp8", 16, seed=23 + k)
+        ref = s.call()
+        torch.cuda.synchronize()
+        out = torch.empty_like(ref)
+        ws = torch.empty(bat.bat_kv_attention_workspace_bytes(s.T, 8, 2, 128, seqs[0][0]), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.call(out=out, workspace=ws)
+        calls.append((s, ref, out, ws, g, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for _, _, out, _, _, _ in calls:
+            out.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for _, _, _, _, g, st in calls:
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for _, ref, out, _, _, _ in calls:
+            assert torch.equal(out, ref)
+
+
+def test_attention_right_after_the_store(bat):
+    """Store, attend, overwrite and attend again without a wait between: each call sees its own cache."""
+    for n in (1, 60):
+        s = Setup(bat, [(n, 400)], 8, 2, 128, "mxfp8", 16, seed=25)
+        eyeA, eyeB = torch.eye(8).cuda(), torch.eye(4).repeat(4, 1, 1).cuda()
+        j = torch.arange(400)
+        slot = (s.table[0].cpu()[j // 16].long() * 16 + j % 16).cuda()
+        g = torch.Generator().manual_seed(26)
+        xs = [torch.randn(400, 2, 128, generator=g).bfloat16().cuda() for _ in range(6)]
+        alone = []
+        for x in xs:
+            bat.bat_kv_quantize(x, eyeA, eyeB, slot, s.caches[0])
+            bat.bat_kv_quantize(x, eyeA, eyeB, slot, s.caches[1])
+            torch.cuda.synchronize()
+            alone.append(s.call())
+            torch.cuda.synchronize()
+        for _ in range(5):
+            got = []
+            for x in xs:
+                bat.bat_kv_quantize(x, eyeA, eyeB, slot, s.caches[0])
+                bat.bat_kv_quantize(x, eyeA, eyeB, slot, s.caches[1])
+                got.append(s.call())
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, alone))

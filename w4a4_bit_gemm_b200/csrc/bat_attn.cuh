@@ -438,7 +438,9 @@ __device__ __forceinline__ void attn_block_apply(const AttnFactors& f, int blk, 
 // the largest scale exponent of a token, the weights are taken as
 //   w = 2^(x + E - M),  M the running maximum of x + E  (x: the score in log2 units),
 // and multiplied by 2^(e_b - E) <= 1 for block b, so V's codes enter the product as they are.
-// Bound: HBM bytes for KV8, about equally the issue slots for KV4.
+// Bound: latency for KV8 (two warps a scheduler; 3.4 to 3.9 TB/s of the measured 6.5), the instructions for
+// KV4 (846 a warp and tile): 8 x 65536 tokens of 8 heads of 128 in 224 us (2.5 TB/s). A step of 16
+// sequences of up to 4096 tokens: 40 us, 8 of them a unit's start (look-ups, q, first copies).
 template <bool kFp8, int kNB>
 struct AttnRowCfg {
   static constexpr int kTok = 32;                            // tokens of a warp's tile

@@ -24,8 +24,10 @@
 // this one: the softmax waits less, but a kind::f16 MMA takes about 120 cycles with N = 64 as with 128,
 // and a 2048-token chunk over 16384 ran 801 us instead of 717. The weights' sum as the test of the
 // reference instead of the maximum: 758 us.)
-// What bounds it: the tensor pipe and the exponentials' unit about equally (a chunk of 256
-// rows: 2048 cycles of MMA at the nominal rate, 2048 cycles of 16 exponentials a cycle).
+// What bounds it: latency along a chunk's chain (scores, softmax, P V, next scores), with the tensor pipe
+// and the exponentials' unit each about 31 % busy. 2048 new tokens over 16384 (32 / 8 heads of 128, KV8):
+// 707 us, 728 TFLOP/s, 0.44 of a cuBLAS bf16 product's rate; about 5900 cycles a chunk of 256 rows where
+// MMAs and exponentials at their nominal rates would take 2048 each.
 //
 // A NaN in V must not reach rows that do not see its token, but 0 times NaN in the MMA would
 // carry it there: the loader stores 0 in its place and notes (token, block);
