@@ -749,13 +749,16 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
             put(stage, b * kBatch + k, x);
           }
           if (kv == 1 && (nan & 0x80808080u) != 0u) {
-            // the rare way round: the pieces with a NaN again, with 0 in its place, and a note
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-              const int tk = 16 * lw + (b * kBatch + k) * kTpi + sub;
-              const uint32_t w[4] = {src[k].x, src[k].y, src[k].z, src[k].w};
+            // the rare way round: the pieces with a NaN again (from the cache), with 0 in its place,
+            // and a note
+#pragma unroll 1
+            for (int k = b * kBatch; k < (b + 1) * kBatch; ++k) {
+              const int tk = 16 * lw + k * kTpi + sub;
               const uint32_t f = ix.fac[1][tk][pblk];
               const bool all = f == 0x7FFF7FFFu;
+              const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+                  p.v_codes + piece_off + static_cast<uint64_t>(ix.row[tk]) * static_cast<uint32_t>(row_bytes)));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
               uint32_t x[kX], any = 0u;
 #pragma unroll
               for (int q = 0; q < kX; ++q) x[q] = 0u;
@@ -771,10 +774,10 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
                 }
               }
               if (any != 0u || all) {
-                put(stage, b * kBatch + k, x);
+                put(stage, k, x);
                 if (has) {
                   atomicOr(&note.tok[tk], 1u << pblk);
-                  note.any[lw] = 1;
+                  note.any[tk >> 4] = 1;
                 }
               }
             }
