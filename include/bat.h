@@ -352,8 +352,9 @@ typedef struct {
  *              the device, at the time the kernels run: a captured call may be replayed with
  *              other values. A length over max_pages * page_size (or 2^30, or below 0) and
  *              a start outside [0, T] are clamped and set the device error word.
- *   max_q_len: the largest n_b that the call may meet (host value; it picks the kernel and
- *              the workspace's size; results are right for longer chunks too).
+ *   max_q_len: the largest n_b that the call may meet (host value; with T, H, D and the table's
+ *              capacity it picks the kernel, and the workspace's size; results are right for
+ *              longer chunks too).
  *   scale    : finite; usually 1 / sqrt(D).
  *   window   : 0 for none, else >= 1; sinks >= 0 (first tokens that stay visible behind the
  *              window; without a window they change nothing).

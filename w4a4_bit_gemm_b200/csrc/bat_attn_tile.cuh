@@ -23,7 +23,8 @@
 // (Tried and not kept: S in halves of 64 tokens, the next chunk's first half computed before P V of
 // this one: the softmax waits less, but a kind::f16 MMA takes about 120 cycles with N = 64 as with 128,
 // and a 2048-token chunk over 16384 ran 801 us instead of 717. The weights' sum as the test of the
-// reference instead of the maximum: 758 us.)
+// reference instead of the maximum: 758 us. An issuing warp for each tile: 848 us, the tiles' MMAs then
+// cut into each other. Without any softmax, stores or loads the MMAs and their hand-offs alone take 535.)
 // What bounds it: latency along a chunk's chain (scores, softmax, P V, next scores), with the tensor pipe
 // and the exponentials' unit each about 31 % busy. 2048 new tokens over 16384 (32 / 8 heads of 128, KV8):
 // 707 us, 728 TFLOP/s, 0.44 of a cuBLAS bf16 product's rate; about 5900 cycles a chunk of 256 rows where
