@@ -362,6 +362,7 @@ typedef struct {
  *              (device fp32 [s][s] and [D/32][32/s][32/s]), or both NULL for none.
  *   out      : bf16 [T][Hq][D] contiguous, 16-byte aligned. A row that sees nothing gives 0.
  *              Tokens behind q_starts[B] are left as they were.
+ *              out and lse must not overlap any input or the workspace.
  *   lse      : fp32 [T][Hq] or NULL: ln sum_j exp(s_j); -inf for a row that sees nothing.
  *   workspace: device, >= bat_kv_attention_workspace_bytes(...) bytes, 256-byte aligned,
  *              its contents unused after the call. Calls that may overlap on the GPU need
