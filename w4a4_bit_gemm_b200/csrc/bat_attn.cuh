@@ -281,6 +281,18 @@ __device__ __forceinline__ float attn_exp2(float x) {
   return r;
 }
 
+// (a NaN among the operands is passed over)
+__device__ __forceinline__ float attn_max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float attn_min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // ---------------------------------------------------------------- stored elements -> f16, bf16
 // f16 takes two codes from one conversion instruction, exactly, and gives q P_q and the weights 11
 // significant bits instead of bf16's 8. Its narrow range is no limit where both sides of a sum
@@ -338,6 +350,15 @@ __device__ __forceinline__ void attn_mma_f16(float (&d)[4], uint32_t a0, uint32_
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same on bf16 operands.
+__device__ __forceinline__ void attn_mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t attn_mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -370,6 +391,15 @@ __device__ __forceinline__ uint32_t attn_transpose8(uint32_t x) {
 __device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A pair of f16 code values (at most 4 significant bits) as bf16.
+__device__ __forceinline__ uint32_t attn_f16_to_bf16(uint32_t x) {
+  float lo, hi;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(x));
+  return attn_pack(lo, hi);
 }
 
 // ---------------------------------------------------------------- block transforms
@@ -436,8 +466,12 @@ __device__ __forceinline__ void attn_block_apply(const AttnFactors& f, int blk, 
 // the lengths. A lane looks up one token of the tile, its page, row and scales.
 // Scales: S^T of each 32-channel block is multiplied by the tokens' K scales in fp32. For V, with E
 // the largest scale exponent of a token, the weights are taken as
-//   w = 2^(x + E - M),  M the running maximum of x + E  (x: the score in log2 units),
+//   w = 2^(x + E - M + 13),  M the running maximum of x + E  (x: the score in log2 units),
 // and multiplied by 2^(e_b - E) <= 1 for block b, so V's codes enter the product as they are.
+// Both are f16 where every factor w 2^(e_b - E) of the tile is a normal f16 number (2^-14 and more: x + E
+// within 2^27 of M for blocks of one size), which keeps the weights' 11 bits. A tile where one is not, be it a
+// weight far below the maximum or a block far below its token's largest, takes the wide way: the
+// weights as the sum of two bf16 numbers (16 bits, fp32's range), twice the products.
 // Bound: latency for KV8 (two warps a scheduler; 3.4 to 3.9 TB/s of the measured 6.5), the instructions for
 // KV4 (846 a warp and tile): 8 x 65536 tokens of 8 heads of 128 in 224 us (2.5 TB/s). A step of 16
 // sequences of up to 4096 tokens: 40 us, 8 of them a unit's start (look-ups, q, first copies).
@@ -451,8 +485,8 @@ struct AttnRowCfg {
   static constexpr int kVs = kBytes + 16;
   static constexpr int kStages = !kFp8 && kNB == 2 ? 3 : 2;
   static constexpr int kStageBytes = kTok * (kKs + kVs);
-  // factors of a tile: K scales fp32 [32][kNB], V factors f16 [kNB][32], E fp32 [32]
-  static constexpr int kFacBytes = kTok * kNB * 4 + kTok * kNB * 2 + kTok * 4;
+  // factors of a tile: K scales fp32 [32][kNB], V factors f16 [kNB][32], E fp32 [32], the spread
+  static constexpr int kFacBytes = kTok * kNB * 4 + kTok * kNB * 2 + kTok * 4 + 16;
   static constexpr int kWarpBytes = kStages * kStageBytes + 2 * kFacBytes;
 };
 constexpr size_t attn_rows_ring_bytes(int warp_bytes, int nt, int nb) {
@@ -570,26 +604,24 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     // the lane's token's scale bytes, four a word
     constexpr int kW = (kNB + 3) / 4;
     uint32_t sck[kW], scv[kW];
-    auto load_scales = [&](int row) {
-      const int64_t at = static_cast<int64_t>(max(row, 0)) * p.nb;
+    auto scale_bytes = [&](const uint8_t* scales, int row, uint32_t (&sc)[kW]) {
+      const uint8_t* src = scales + static_cast<int64_t>(max(row, 0)) * p.nb;
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
-        sck[w] = scv[w] = 0u;
+        sc[w] = 0u;
         if (row < 0) continue;
         if (p.scale_words) {
-          if (4 * w < p.nb) {
-            sck[w] = __ldg(reinterpret_cast<const uint32_t*>(p.k_scales + at) + w);
-            scv[w] = __ldg(reinterpret_cast<const uint32_t*>(p.v_scales + at) + w);
-          }
+          if (4 * w < p.nb) sc[w] = __ldg(reinterpret_cast<const uint32_t*>(src) + w);
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (4 * w + k < p.nb) {
-              sck[w] |= static_cast<uint32_t>(__ldg(p.k_scales + at + 4 * w + k)) << (8 * k);
-              scv[w] |= static_cast<uint32_t>(__ldg(p.v_scales + at + 4 * w + k)) << (8 * k);
-            }
+            if (4 * w + k < p.nb) sc[w] |= static_cast<uint32_t>(__ldg(src + 4 * w + k)) << (8 * k);
         }
       }
+    };
+    auto load_scales = [&](int row) {
+      scale_bytes(p.k_scales, row, sck);
+      scale_bytes(p.v_scales, row, scv);
     };
     auto put_scales = [&](int par) {
       float* fk = reinterpret_cast<float*>(facs + par * C::kFacBytes);
@@ -601,12 +633,13 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
         nan |= (((sck[w] & 0x7F7F7F7Fu) + 0x01010101u) & sck[w]) | (((scv[w] & 0x7F7F7F7Fu) + 0x01010101u) & scv[w]);
       nan &= 0x80808080u;
       float kf[kNB];
-      int top = 0;
+      int top = 0, low = 255;
 #pragma unroll
       for (int b = 0; b < kNB; ++b) {
         const int ek = (sck[b / 4] >> (8 * (b & 3))) & 255u, ev = (scv[b / 4] >> (8 * (b & 3))) & 255u;
         kf[b] = __uint_as_float(max(static_cast<uint32_t>(ek) << 23, 0x00400000u));  // (byte 0: 2^-127)
         top = max(top, ev);
+        low = min(low, (ev - 1) & 255);  // (byte 0 last)
       }
       if (nan) {
         top = 0;
@@ -637,6 +670,10 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
       for (int b = 0; b < kNB; b += 2)
         *reinterpret_cast<float2*>(fk + lane * kNB + b) = make_float2(kf[b], kf[b + 1]);
       fe[lane] = static_cast<float>(top - 127);
+      // the tile's spread, the largest E - e_b of a token (blocks of scale byte 0, in practice all
+      // zeros, do not count), less the bits below M that f16 has
+      const unsigned spread = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(max(top - 1 - low, 0)));
+      if (lane == 0) fe[C::kTok] = static_cast<float>(static_cast<int>(spread) - 27);
     };
 
     int rw[kS + 1];  // cache rows of tiles i .. i + kS - 1 of the warp, a token a lane
@@ -716,7 +753,7 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     put_scales(0);
     load_scales(rw[1]);
 
-    // m, M: running references of the scores and of score + E (within 2^8 of the maxima)
+    // m, M: running references of the scores and of score + E (within 2^8 and 2^2 of the maxima)
     float m[kNT][2], mv[kNT][2], l[kNT][2], o[kNT][2 * kNB][4];
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
@@ -784,56 +821,115 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
         e[u][0] = fe[16 * u + r];
         e[u][1] = fe[16 * u + r + 8];
       }
-      uint32_t pb[2][kNT][2];
+      // A normal f16 factor needs x + E - M + 13 - (E - e_b) >= -14. (Tokens that are not there: -inf + inf is
+      // NaN, which the minimum and the maximum pass over.)
+      float el[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        el[u][0] = there >> (16 * u + r) & 1u ? e[u][0] : INFINITY;
+        el[u][1] = there >> (16 * u + r + 8) & 1u ? e[u][1] : INFINITY;
+      }
+      const float reach = fe[C::kTok];
+      bool far[kNT][2], wide = false;  // columns that go the wide way; any of the warp's
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
-        float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
+        float top[2], topv[2], low[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float& x = s[u][t][k];
-            x = there >> (16 * u + r + 8 * (k >> 1)) & 1u ? x * cs[t][k & 1] : -INFINITY;
-            top[k & 1] = fmaxf(top[k & 1], x);
-            topv[k & 1] = fmaxf(topv[k & 1], x + e[u][k >> 1]);
+          for (int k = 0; k < 2; ++k) {
+            float &x0 = s[u][t][k], &x1 = s[u][t][k + 2];
+            x0 = there >> (16 * u + r) & 1u ? x0 * cs[t][k] : -INFINITY;
+            x1 = there >> (16 * u + r + 8) & 1u ? x1 * cs[t][k] : -INFINITY;
+            const float e0 = x0 + el[u][0], e1 = x1 + el[u][1];
+            top[k] = u ? attn_max3(top[k], x0, x1) : fmaxf(x0, x1);
+            topv[k] = u ? attn_max3(topv[k], e0, e1) : fmaxf(e0, e1);
+            low[k] = u ? attn_min3(low[k], e0, e1) : fminf(e0, e1);
           }
-        const bool up = top[0] > m[t][0] + 8.0f || top[1] > m[t][1] + 8.0f || topv[0] > mv[t][0] + 8.0f ||
-                        topv[1] > mv[t][1] + 8.0f;
-        if (__any_sync(0xffffffffu, up)) {
-          float f[2];
+        const bool up = top[0] > m[t][0] + 8.0f || top[1] > m[t][1] + 8.0f || topv[0] > mv[t][0] + 2.0f ||
+                        topv[1] > mv[t][1] + 2.0f;
+        far[t][0] = low[0] < mv[t][0] + reach;
+        far[t][1] = low[1] < mv[t][1] + reach;
+        if (__any_sync(0xffffffffu, up || far[t][0] || far[t][1])) {
+          if (__any_sync(0xffffffffu, up)) {
+            float f[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) {
+                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
+                topv[k] = fmaxf(topv[k], __shfl_xor_sync(0xffffffffu, topv[k], d));
+              }
+              top[k] = fmaxf(m[t][k], top[k]);
+              topv[k] = fmaxf(mv[t][k], topv[k]);
+              l[t][k] *= top[k] == -INFINITY ? 1.0f : attn_exp2(m[t][k] - top[k]);
+              f[k] = topv[k] == -INFINITY ? 1.0f : attn_exp2(mv[t][k] - topv[k]);
+              m[t][k] = top[k];
+              mv[t][k] = topv[k];
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * kNB; ++i) {
+              o[t][i][0] *= f[0];
+              o[t][i][1] *= f[1];
+              o[t][i][2] *= f[0];
+              o[t][i][3] *= f[1];
+            }
+          }
+          // (a column's way goes by its own scores and the tokens' scales, not by the other heads)
+          const unsigned mine = 0x11111111u << c;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-              top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
-              topv[k] = fmaxf(topv[k], __shfl_xor_sync(0xffffffffu, topv[k], d));
-            }
-            top[k] = fmaxf(m[t][k], top[k]);
-            topv[k] = fmaxf(mv[t][k], topv[k]);
-            l[t][k] *= top[k] == -INFINITY ? 1.0f : attn_exp2(m[t][k] - top[k]);
-            f[k] = topv[k] == -INFINITY ? 1.0f : attn_exp2(mv[t][k] - topv[k]);
-            m[t][k] = top[k];
-            mv[t][k] = topv[k];
-          }
-#pragma unroll
-          for (int i = 0; i < 2 * kNB; ++i) {
-            o[t][i][0] *= f[0];
-            o[t][i][1] *= f[1];
-            o[t][i][2] *= f[0];
-            o[t][i][3] *= f[1];
+            const unsigned any = __ballot_sync(0xffffffffu, low[k] < mv[t][k] + reach);
+            far[t][k] = (any & mine) != 0u;
+            wide |= any != 0u;
           }
         }
+      }
+      // V of block b, half u of the tile, as f16: channel 4 r + k: tokens (2c, 2c + 1), (2c + 8, 2c + 9)
+      auto load_v = [&](int b, int u, uint32_t (&v)[4][2]) {
+        const uint8_t* src = vt + (16 * u + 2 * c) * C::kVs;
+        if (kFp8) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t w0 = *reinterpret_cast<const uint32_t*>(src + 8 * x * C::kVs + 32 * b + 4 * r);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t*>(src + (8 * x + 1) * C::kVs + 32 * b + 4 * r);
+            attn_e4m3_f16(__byte_perm(w0, w1, 0x5140), v[0][x], v[1][x]);
+            attn_e4m3_f16(__byte_perm(w0, w1, 0x7362), v[2][x], v[3][x]);
+          }
+        } else {
+          // nibbles of the same channel side by side: even channels, odd channels
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = *reinterpret_cast<const uint16_t*>(src + ((x & 1) + 8 * (x >> 1)) * C::kVs + 16 * b + 2 * r);
+          const uint32_t a = w[0] | w[2] << 16, d = w[1] | w[3] << 16;
+          uint32_t ev[4], od[4];
+          attn_e2m1_f16((a & 0x0F0F0F0Fu) | ((d << 4) & 0xF0F0F0F0u), ev);
+          attn_e2m1_f16(((a >> 4) & 0x0F0F0F0Fu) | (d & 0xF0F0F0F0u), od);
+          v[0][0] = ev[0];
+          v[2][0] = ev[1];
+          v[0][1] = ev[2];
+          v[2][1] = ev[3];
+          v[1][0] = od[0];
+          v[3][0] = od[1];
+          v[1][1] = od[2];
+          v[3][1] = od[3];
+        }
+      };
+      uint32_t pb[2][kNT][2];
+#pragma unroll
+      for (int t = 0; t < kNT; ++t) {
         float ms[2], vs[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           ms[k] = m[t][k] == -INFINITY ? 0.0f : m[t][k];
-          vs[k] = mv[t][k] == -INFINITY ? 0.0f : mv[t][k];
+          vs[k] = far[t][k] ? INFINITY : (mv[t][k] == -INFINITY ? 0.0f : mv[t][k] - 13.0f);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           l[t][0] += attn_exp2(s[u][t][0] - ms[0]) + attn_exp2(s[u][t][2] - ms[0]);
           l[t][1] += attn_exp2(s[u][t][1] - ms[1]) + attn_exp2(s[u][t][3] - ms[1]);
-          // weights in f16 (half a step 2^-11 of each); their sum l keeps fp32
+          // weights up to 2^15 in f16 (off by half a step, 2^-11 of each); their sum l keeps fp32
           pb[u][t][0] = attn_transpose8(attn_pack_f16(attn_exp2(s[u][t][0] + (e[u][0] - vs[0])),
                                                       attn_exp2(s[u][t][1] + (e[u][0] - vs[1]))));
           pb[u][t][1] = attn_transpose8(attn_pack_f16(attn_exp2(s[u][t][2] + (e[u][1] - vs[0])),
@@ -847,40 +943,79 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint2 f = *reinterpret_cast<const uint2*>(fv + b * 32 + 16 * u + 4 * c);
-          uint32_t v[4][2];  // channel 4 r + k: tokens (2c, 2c + 1), (2c + 8, 2c + 9)
-          const uint8_t* src = vt + (16 * u + 2 * c) * C::kVs;
-          if (kFp8) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t w0 = *reinterpret_cast<const uint32_t*>(src + 8 * x * C::kVs + 32 * b + 4 * r);
-              const uint32_t w1 = *reinterpret_cast<const uint32_t*>(src + (8 * x + 1) * C::kVs + 32 * b + 4 * r);
-              attn_e4m3_f16(__byte_perm(w0, w1, 0x5140), v[0][x], v[1][x]);
-              attn_e4m3_f16(__byte_perm(w0, w1, 0x7362), v[2][x], v[3][x]);
-            }
-          } else {
-            // nibbles of the same channel side by side: even channels, odd channels
-            uint32_t w[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              w[x] = *reinterpret_cast<const uint16_t*>(src + ((x & 1) + 8 * (x >> 1)) * C::kVs + 16 * b + 2 * r);
-            const uint32_t a = w[0] | w[2] << 16, d = w[1] | w[3] << 16;
-            uint32_t ev[4], od[4];
-            attn_e2m1_f16((a & 0x0F0F0F0Fu) | ((d << 4) & 0xF0F0F0F0u), ev);
-            attn_e2m1_f16(((a >> 4) & 0x0F0F0F0Fu) | (d & 0xF0F0F0F0u), od);
-            v[0][0] = ev[0];
-            v[2][0] = ev[1];
-            v[0][1] = ev[2];
-            v[2][1] = ev[3];
-            v[1][0] = od[0];
-            v[3][0] = od[1];
-            v[1][1] = od[2];
-            v[3][1] = od[3];
-          }
+          uint32_t v[4][2];
+          load_v(b, u, v);
 #pragma unroll
           for (int t = 0; t < kNT; ++t) {
             const uint32_t q0 = attn_mul_f16x2(pb[u][t][0], f.x), q1 = attn_mul_f16x2(pb[u][t][1], f.y);
             attn_mma_f16(o[t][2 * b], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
             attn_mma_f16(o[t][2 * b + 1], v[2][0], v[3][0], v[2][1], v[3][1], q0, q1);
+          }
+        }
+      }
+      if (__builtin_expect(wide, 0)) {
+        // ---- the wide way, for the columns that take it (the others' weights are 0)
+        uint32_t mine[kW];  // the token's V scales again
+        scale_bytes(p.v_scales, rw[0], mine);
+        int top = 0;
+#pragma unroll
+        for (int b = 0; b < kNB; ++b) {
+          const int ev = (mine[b / 4] >> (8 * (b & 3))) & 255u;
+          top = ev != 255 ? max(top, ev) : top;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          // top and scale bytes of this lane's four tokens
+          int tt[4];
+          uint32_t sv[4][kW];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int src = 16 * u + 2 * c + (x & 1) + 8 * (x >> 1);
+            tt[x] = __shfl_sync(0xffffffffu, top, src);
+#pragma unroll
+            for (int w = 0; w < kW; ++w) sv[x][w] = __shfl_sync(0xffffffffu, mine[w], src);
+          }
+          uint32_t hi[kNT][2], lo[kNT][2];
+#pragma unroll
+          for (int t = 0; t < kNT; ++t) {
+            float w[4], vs[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) vs[k] = far[t][k] ? mv[t][k] - 13.0f : INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = attn_exp2(s[u][t][k] + (e[u][k >> 1] - vs[k & 1]));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t h = attn_pack(w[2 * x], w[2 * x + 1]);
+              hi[t][x] = attn_transpose8(h);
+              lo[t][x] = attn_transpose8(attn_pack(w[2 * x] - bf16lo(h), w[2 * x + 1] - bf16hi(h)));
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < kNB; ++b) {
+            if (b >= p.nb) break;
+            uint32_t v[4][2], f[2];
+            load_v(b, u, v);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t h[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const int ev = (sv[2 * x + k][b / 4] >> (8 * (b & 3))) & 255u, d = tt[2 * x + k] - ev;
+                h[k] = ev == 255 ? 0x7FFFu : static_cast<uint32_t>(max(127 - d, 0)) << 7;  // 2^-d
+              }
+              f[x] = h[0] | h[1] << 16;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) v[k][x] = attn_f16_to_bf16(v[k][x]);
+            }
+#pragma unroll
+            for (int t = 0; t < kNT; ++t)
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                const uint32_t q0 = attn_mul_bf16x2(g ? lo[t][0] : hi[t][0], f[0]);
+                const uint32_t q1 = attn_mul_bf16x2(g ? lo[t][1] : hi[t][1], f[1]);
+                attn_mma_bf16(o[t][2 * b], v[0][0], v[1][0], v[0][1], v[1][1], q0, q1);
+                attn_mma_bf16(o[t][2 * b + 1], v[2][0], v[3][0], v[2][1], v[3][1], q0, q1);
+              }
           }
         }
       }
@@ -896,12 +1031,14 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     // ---- join the warps
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
-      float f[2];
+      float f[2], f2[2];  // 2^(M - 13 - m) in two factors (its exponent may be below fp32's)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
-        f[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(mv[t][k] - m[t][k]);
+        const float d = mv[t][k] - 13.0f - m[t][k], d2 = floorf(0.5f * d);
+        f[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(d - d2);
+        f2[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(d2);
         if (r == 0) {
           float* ml = sml + (warp * kR + 8 * t + 2 * c + k) * 2;
           ml[0] = m[t][k];
@@ -913,8 +1050,8 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
         // rows r and r + 8 of m-tile i are channels 32 (i / 2) + 4 r + 2 (i % 2) and the next
         const int d = 32 * (i >> 1) + 4 * r + 2 * (i & 1);
         float* o0 = so + (warp * kR + 8 * t + 2 * c) * kLdo + d;
-        *reinterpret_cast<float2*>(o0) = make_float2(o[t][i][0] * f[0], o[t][i][2] * f[0]);
-        *reinterpret_cast<float2*>(o0 + kLdo) = make_float2(o[t][i][1] * f[1], o[t][i][3] * f[1]);
+        *reinterpret_cast<float2*>(o0) = make_float2(o[t][i][0] * f[0] * f2[0], o[t][i][2] * f[0] * f2[0]);
+        *reinterpret_cast<float2*>(o0 + kLdo) = make_float2(o[t][i][1] * f[1] * f2[1], o[t][i][3] * f[1] * f2[1]);
       }
     }
     __syncthreads();
