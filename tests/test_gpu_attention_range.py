@@ -85,3 +85,73 @@ def test_v_tiny_and_large_scales(bat, fmt, seqs):
         if by == -100 and seqs[0][0] > 1:
             continue  # (chunks hold products in units of 2^-32 of fp32's range: see the header)
         c.check()
+
+# ------------------------------------------------------------------ keys that differ in size
+def _same_rows(bat, fmt, seqs, change, rows, D=128, **kw):
+    """`change`s the keys of tokens that `rows` do not see: their bits stay."""
+    c = Case(bat, seqs, 8, 2, D, fmt, seed=4)
+    ref, rl = c.check(**kw)
+    change(c.K)
+    out, lse = c.call(**kw)
+    assert torch.equal(out[rows], ref[rows]) and torch.equal(lse[rows], rl[rows])
+
+
+@FMT
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("up", [14, 24, 40, 120])
+def test_k_of_a_later_token(bat, fmt, D, up):
+    """The last new token's key is far larger: the rows before it do not see it."""
+    def change(K):
+        K.scales[259] += up
+    _same_rows(bat, fmt, [(100, 260)], change, slice(0, 99), D)
+
+
+@FMT
+@pytest.mark.parametrize("up", [24, 120])
+def test_k_of_a_token_before_the_window(bat, fmt, up):
+    def change(K):
+        K.scales[170] += up
+    # row i at position 160 + i sees 170 from i = 10 to 10 + 49
+    _same_rows(bat, fmt, [(100, 260)], change, slice(60, 100), window=50, sinks=3)
+
+
+@FMT
+@SEQS
+@pytest.mark.parametrize("up", [18, 26, 60])
+def test_k_of_a_token_far_below_the_others_weight(bat, fmt, seqs, up):
+    """A key far larger than its neighbours, against the rows' direction: its weight is 0 and the
+    neighbours' scores count."""
+    T = sum(n for n, _ in seqs)
+    g = torch.Generator().manual_seed(5)
+    c = Case(bat, seqs, 4, 2, 128, fmt, seed=6, q=0.2 + torch.rand(T, 4, 128, generator=g))
+    c.K.codes[20] = 0x80 | 0x70 if fmt == "mxfp8" else 8 | 6
+    c.K.scales[20] += up
+    c.check()
+
+
+@FMT
+@SEQS
+@pytest.mark.parametrize("up", [17, 30])
+def test_k_blocks_of_a_token_apart(bat, fmt, seqs, up):
+    """The first block of every key is far larger and meets zeros in q: the others decide."""
+    T = sum(n for n, _ in seqs)
+    g = torch.Generator().manual_seed(7)
+    q = torch.randn(T, 8, 128, generator=g)
+    q[..., :32] = 0
+    c = Case(bat, seqs, 8, 2, 128, fmt, seed=8, q=q)
+    c.K.shift((slice(None), slice(None), 0), up)
+    c.check()
+
+
+@FMT
+def test_k_zero_blocks(bat, fmt):
+    """Blocks of zeros (scale byte 0, as the store writes them) beside ordinary ones."""
+    c = Case(bat, [(60, 300)], 4, 2, 128, fmt, seed=9)
+    for st in (c.K, c.V):
+        st.codes[:, 0, 96:] = 0
+        st.scales[:, 0, 3] = 0
+        st.codes[5:90, 1] = 0
+        st.scales[5:90, 1] = 0
+    c.check()
+
+

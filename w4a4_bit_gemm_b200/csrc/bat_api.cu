@@ -1230,6 +1230,7 @@ bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int64_t q_st
   ws += round_up(ctas * static_cast<int64_t>(sizeof(bat::AttnMark)), 256);
   if (tile) {
     uint16_t* qt = reinterpret_cast<uint16_t*>(ws);
+    p.qt = qt;
     p.qt_fac = reinterpret_cast<const float*>(ws + round_up(T * Hq * D * 2, 256));
     if (D > 128)
       return fp8 ? launch_attn_tile<true, 256>(p, qt, dev, sms, 9, s) : launch_attn_tile<false, 256>(p, qt, dev, sms, 10, s);

@@ -83,7 +83,8 @@ struct AttnParams {
   int scale_words;         // the scale arrays may be read by 32-bit words (nb % 4 == 0, aligned)
   float scale_log2;        // |scale| * log2(e)
   float q_sign;            // sign of the scale, taken into q
-  const float* qt_fac;     // tile kernel: factors of the prepared q rows, [Hkv][T][G]
+  const uint16_t* qt;      // tile kernel: prepared q rows, f16 [Hkv][T][G][D]
+  const float* qt_fac;     // and their factors, [Hkv][T][G]
 };
 
 // One sequence's facts, from the device arrays, made safe: n >= 0, tokens inside [0, T),
@@ -298,8 +299,8 @@ __device__ __forceinline__ float attn_min3(float a, float b, float c) {
 // significant bits instead of bf16's 8. Its narrow range is no limit where both sides of a sum
 // are scaled by powers of two: a row of q by its largest channel; in the row kernel the scores of
 // each 32-channel block by its MX scale in fp32, and V through the weights (below); in the
-// tile kernel K by the largest scale of its chunk, so that what falls below f16's range is below
-// 2^-25 of the chunk's largest products. The tile kernel's V goes to bf16, whose range is
+// tile kernel K by the largest scale of 16 neighbouring tokens where f16 then holds all their codes, by
+// each token's own largest where it does not. The tile kernel's V goes to bf16, whose range is
 // fp32's: there the weights cannot take its scales up.
 __device__ __forceinline__ uint32_t attn_mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -393,12 +394,15 @@ __device__ __forceinline__ uint32_t attn_pack(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// A pair of f16 code values (at most 4 significant bits) as bf16.
-__device__ __forceinline__ uint32_t attn_f16_to_bf16(uint32_t x) {
-  float lo, hi;
+__device__ __forceinline__ void attn_f16_floats(uint32_t x, float& lo, float& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
       : "=f"(lo), "=f"(hi)
       : "r"(x));
+}
+// A pair of f16 code values (at most 4 significant bits) as bf16.
+__device__ __forceinline__ uint32_t attn_f16_to_bf16(uint32_t x) {
+  float lo, hi;
+  attn_f16_floats(x, lo, hi);
   return attn_pack(lo, hi);
 }
 

@@ -65,21 +65,23 @@ struct Cfg {
 
 // What the loader warps note about a chunk for the softmax warps.
 struct AttnNote {
-  float kfac[8];      // 2^(largest K scale of the warp's 16 tokens)
-  int any[8];         // some of its tokens are hidden (bad page) or hold a NaN in V
-  uint32_t tok[128];  // bit 31: hidden; bit b: NaN in V's block b
+  float kfac[8];      // 2^(largest K scale of the warp's 16 tokens), 1 where they are apart
+  int any[8];         // of its tokens: kNoteSome some are hidden (bad page) or hold a NaN in V, kNoteApart
+                      // their K scales are too far apart for one factor, kNoteWide a token's own are
+  uint32_t tok[128];  // bit 31: hidden; bit 30: wide; bits 16-23: scale byte of the token's K column (127:
+                      // none); bit b: NaN in V's block b
 };
+constexpr int kNoteSome = 1, kNoteApart = 2, kNoteWide = 4;
 // A chunk's cache rows (0 for none) and factors (16-bit pairs) for the loader warps.
 template <int kNB>
 struct AttnIndex {
   uint32_t row[128];
   uint32_t fac[2][128][kNB];  // K, V
 };
-__device__ __forceinline__ bool attn_note_any(const AttnNote& n) {
+__device__ __forceinline__ int attn_note_any(const AttnNote& n) {
   const volatile int4* a = reinterpret_cast<const volatile int4*>(n.any);
-  return (a[0].x | a[0].y | a[0].z | a[0].w | a[1].x | a[1].y | a[1].z | a[1].w) != 0;
+  return a[0].x | a[0].y | a[0].z | a[0].w | a[1].x | a[1].y | a[1].z | a[1].w;
 }
-
 // idesc of kind::f16, fp32 accumulation, A K-major; kBf16: both operands bf16, else f16;
 // kMnB: B is MN-major.
 template <bool kBf16, bool kMnB>
@@ -127,6 +129,72 @@ __device__ __forceinline__ void attn_tmem_ld16(uint32_t taddr, uint32_t (&r)[16]
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
+}
+
+// One column.
+__device__ __forceinline__ void attn_tmem_st1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
+
+// The scores of a chunk's tokens whose K scales are too far apart for one factor (rare; the whole warp calls it): the
+// columns that were taken by the token's own scale, times that scale, a power of two: exact; and those of tokens
+// whose own blocks are too far apart, a block at a time in fp32 on the CUDA cores. qrow: the lane's row among the
+// prepared q rows, or -1. (Out of line, for the softmax loop's sake.)
+template <bool kFp8>
+__device__ __noinline__ void attn_far_keys(const AttnParams& p, const AttnNote& note, uint32_t taddr, int64_t qrow, int b,
+                                           int h, AttnSpan span, int i0) {
+#pragma unroll 1
+  for (int k = 0; k < 128; k += 16) {
+    if (!(note.any[k >> 4] & kNoteApart)) continue;
+    uint32_t s[16];
+    attn_tmem_ld16(taddr + k, s);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float x = __uint_as_float(s[j]), y = x * attn_scale_value(note.tok[k + j] >> 16 & 255u);
+      s[j] = __float_as_uint(fabsf(y) == INFINITY && fabsf(x) != INFINITY ? copysignf(3e38f, x) : y);
+    }
+    tmem_st_32x32b_x16(taddr + k, s);
+  }
+  tmem_wait_st();
+#pragma unroll 1
+  for (int c = 0; c < 128; ++c) {
+    if ((note.tok[c] >> 30) != 1u) continue;  // wide and not hidden
+    float s = 0.0f;
+    if (qrow >= 0) {
+      const int64_t row = attn_cache_row(p, p.table + static_cast<int64_t>(b) * p.max_pages, span.token(i0 + c), h);
+      const uint8_t* codes = p.k_codes + row * (kFp8 ? p.D : p.D / 2);
+      const uint4* q = reinterpret_cast<const uint4*>(p.qt + qrow * p.D);
+#pragma unroll 1
+      for (int blk = 0; blk < p.nb; ++blk) {
+        float d = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {  // 8 channels
+          uint32_t kk[4];
+          if (kFp8) {
+            const uint2 w = *reinterpret_cast<const uint2*>(codes + 32 * blk + 8 * i);
+            attn_e4m3_f16(w.x, kk[0], kk[1]);
+            attn_e4m3_f16(w.y, kk[2], kk[3]);
+          } else {
+            attn_e2m1_f16(*reinterpret_cast<const uint32_t*>(codes + 16 * blk + 4 * i), kk);
+          }
+          const uint4 w = q[4 * blk + i];
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float x0, x1, k0, k1;
+            attn_f16_floats(x[j], x0, x1);
+            attn_f16_floats(kk[j], k0, k1);
+            d = __fmaf_rn(x0, k0, d);
+            d = __fmaf_rn(x1, k1, d);
+          }
+        }
+        s = __fmaf_rn(d, attn_scale_value(p.k_scales[row * p.nb + blk]), s);
+      }
+    }
+    __syncwarp();
+    attn_tmem_st1(taddr + c, s);
+  }
+  tmem_wait_st();
 }
 
 // Channel order that the expansion of V leaves (see attn_e4m3_bits, attn_e2m1_bits): position
@@ -275,7 +343,7 @@ struct AttnRun {
 
 template <bool kFp8, int kDP>
 __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
-    const AttnParams p, const __grid_constant__ CUtensorMap qmap) {
+    const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap) {
   using C = attn_tile::Cfg<kDP>;
   constexpr int kTile = C::kRows, kStages = C::kStages;
   extern __shared__ __align__(16) uint8_t raw[];
@@ -434,15 +502,21 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
         if (!ok) break;
         tc_fence_after();
         // V of the chunk before is complete: its notes
-        if (i > 0 && attn_note_any(notes[(n_c - 1) % attn_tile::kInfo])) see_nan(n_c - 1, chunk - 1);
+        if (i > 0 && (attn_note_any(notes[(n_c - 1) % attn_tile::kInfo]) & kNoteSome)) see_nan(n_c - 1, chunk - 1);
         const AttnNote& note = notes[n_c % attn_tile::kInfo];
         // factor of 16 columns (their tokens share a loader warp)
         auto cc = [&](int g) { return fmaxf(cs * note.kfac[g], 1e-37f); };
         const int i0 = chunk * 128;
         // masked columns go to TMEM as -inf, so that the pass below needs no test
         const bool whole = (i0 >= all_lo || i0 + 128 <= sp.ns) && i0 + 128 <= all_hi;
-        const bool hidden = attn_note_any(note);
-        if (!whole || hidden) {
+        const int some = attn_note_any(note);
+        if (!whole || some) {
+          if (some & (kNoteApart | kNoteWide)) {
+            const int64_t row = static_cast<int64_t>(run.pl.tile) * kTile + 128 * t + rr;
+            const int64_t qrow = (run.pl.hu * p.T + run.seq.t0) * p.G + row;
+            attn_far_keys<kFp8>(p, note, s_col(t) + lane_base, row < static_cast<int64_t>(run.seq.n) * p.G ? qrow : -1,
+                                run.pl.b, run.pl.hu, sp, i0);
+          }
           const int c_hi = v_hi - i0, c_lo = v_lo - i0, c_sink = v_sink - i0;
 #pragma unroll 1
           for (int k = 0; k < 128; k += 32) {
@@ -453,7 +527,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
             for (int j = 0; j < 32; ++j) {
               const int c = k + j;
               if (!(c < c_hi && (c >= c_lo || c < c_sink))) s[j] = 0xFF800000u;
-              if (hidden && (note.tok[c] >> 31)) s[j] = 0xFF800000u;
+              if (some && (note.tok[c] >> 31)) s[j] = 0xFF800000u;
             }
             tmem_st_32x32b_x16(s_col(t) + lane_base + k, reinterpret_cast<const uint32_t(&)[16]>(s[0]));
             tmem_st_32x32b_x16(s_col(t) + lane_base + k + 16, reinterpret_cast<const uint32_t(&)[16]>(s[16]));
@@ -537,7 +611,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
       ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), (n_s - 1) & 1u, kErrWaitTmemFull));
       if (!ok) break;
       tc_fence_after();
-      if (attn_note_any(notes[(n_c - 1) % attn_tile::kInfo])) see_nan(n_c - 1, run.pl.chunk + n - 1);
+      if (attn_note_any(notes[(n_c - 1) % attn_tile::kInfo]) & kNoteSome) see_nan(n_c - 1, run.pl.chunk + n - 1);
       const int64_t row = static_cast<int64_t>(run.pl.tile) * kTile + 128 * t + rr;
       const int64_t rt = row / p.G;
       const bool valid = rt < run.seq.n;
@@ -778,7 +852,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
                 put(stage, k, x);
                 if (has) {
                   atomicOr(&note.tok[tk], 1u << pblk);
-                  note.any[tk >> 4] = 1;
+                  atomicOr(&note.any[tk >> 4], kNoteSome);
                 }
               }
             }
@@ -934,25 +1008,39 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int tk = tk0 + 32 * x;
-            int top = 0;
+            // f16 holds every code times 2^(e - top) for e from top - kReach on
+            constexpr int kReach = kFp8 ? 15 : 23;
+            int own = 0, low = 255;
 #pragma unroll
             for (int b = 0; b < kDP / 32; ++b) {
               const int e = (sck[x][b / 4] >> (8 * (b & 3))) & 255;
-              top = e != 255 ? max(top, e) : top;  // NaN scales do not set the common scale
+              own = e != 255 ? max(own, e) : own;            // NaN scales do not set the common scale
+              low = e != 255 && e != 0 ? min(low, e) : low;  // (byte 0: in practice zeros)
             }
+            int top = own, low16 = low;
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            for (int d = 8; d > 0; d >>= 1) {
+              top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+              low16 = min(low16, __shfl_xor_sync(0xffffffffu, low16, d));
+            }
+            // 16 tokens too far apart for one factor: each by its own largest scale, put right in its column of
+            // scores, so that no token's bits hang on its neighbours; a token that is too far apart in
+            // itself goes without the tensor cores. (Nor has a row's factor times 2^(top - 127) to stay finite
+            // for very large ones.)
+            const bool apart = top - low16 > kReach || top > 200, wide = own - low > kReach;
+            const int ref = apart ? own : top;
 #pragma unroll
             for (int b = 0; b < kDP / 32; ++b) {
               const int ek = (sck[x][b / 4] >> (8 * (b & 3))) & 255, ev = (scv[x][b / 4] >> (8 * (b & 3))) & 255;
-              ix.fac[0][tk][b] = ek == 255 ? 0x7E007E00u : attn_f16_pow2(top - ek);
+              ix.fac[0][tk][b] = ek == 255 ? 0x7E007E00u : attn_f16_pow2(ref - ek);
               ix.fac[1][tk][b] = attn_scale_pair<kFp8>(ev);
             }
-            nt.tok[tk] = bad[x] ? 0x80000000u : 0u;
-            const unsigned any = __ballot_sync(0xffffffffu, bad[x]);
+            nt.tok[tk] = (bad[x] ? 0x80000000u : 0u) | (wide ? 0x40000000u : 0u) | (apart ? own : 127) << 16;
+            const unsigned any = __ballot_sync(0xffffffffu, bad[x]), any_wide = __ballot_sync(0xffffffffu, wide);
             if ((lane & 15) == 0) {
-              nt.kfac[tk >> 4] = attn_scale_value(top);
-              nt.any[tk >> 4] = (any >> (lane & 16) & 0xFFFFu) != 0u;
+              const unsigned half = 0xFFFFu << (lane & 16);
+              nt.kfac[tk >> 4] = apart ? 1.0f : attn_scale_value(top);
+              nt.any[tk >> 4] = (any & half ? kNoteSome : 0) | (apart ? kNoteApart : 0) | (any_wide & half ? kNoteWide : 0);
             }
           }
           __syncwarp();
