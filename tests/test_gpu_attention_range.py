@@ -155,3 +155,16 @@ def test_k_zero_blocks(bat, fmt):
     c.check()
 
 
+
+# ------------------------------------------------------------------ V's largest scales
+@FMT
+@SEQS
+@pytest.mark.parametrize("by", [36, 42, 60, 70])
+def test_v_scales_above_the_usual(bat, fmt, seqs, by):
+    """The same answer from single tokens and from chunks for large stored values."""
+    c = Case(bat, seqs, 4, 2, 64, fmt, seed=10)
+    c.V.shift(slice(None), by)
+    c.check()
+    c = Case(bat, seqs, 4, 2, 64, fmt, seed=11)
+    c.V.shift((slice(2, None, 5), 1, 1), by)
+    c.check()

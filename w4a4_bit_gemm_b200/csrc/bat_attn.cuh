@@ -32,9 +32,10 @@ constexpr int kChunk = 128;   // visible tokens a chunk
 constexpr int kWarps = 4;     // row kernel: warps a CTA, 32 tokens of a chunk each
 constexpr int kThreads = 32 * kWarps;
 // V's stored elements go to bf16 through their bits, which leaves them 2^120 (E4M3) or 2^126
-// (E2M1) too small; the MX scale's multiplication puts that right up to 2^-32, so that
-// scales from 2^-127 to 2^39 (E4M3; 2^33 E2M1) stay within bf16. Outputs are multiplied by 2^32
-// at the end; a product below 2^-94 may be lost to fp32's smallest number.
+// (E2M1) too small; the MX scale's multiplication puts that right up to 2^-32, in one step for
+// scales from 2^-127 to 2^39 (E4M3; 2^33 E2M1), in two for larger ones. Outputs are multiplied by 2^32
+// at the end; a product below 2^-94 may be lost to fp32's smallest number, and with weights of up to 2^40
+// (the tile kernel's reference) sums of values above 2^100 may leave its range.
 constexpr float kUp = 0x1p32f;
 }  // namespace attn
 
@@ -366,11 +367,12 @@ __device__ __forceinline__ uint32_t attn_mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 // Multiplier of a scale byte as a pair of bf16: 2^(byte - 127 + 88) for E4M3, + 94 for E2M1
-// (see kUp). Bytes past the range (see kUp; 255 is NaN by the format) give NaN.
+// (see kUp). 255, NaN by the format, is 0x7FFF; a byte whose multiplier bf16 does not hold is 0x7F80 plus the
+// powers of two above 2^127 that are missing (at most 94).
 template <bool kFp8>
 __device__ __forceinline__ uint32_t attn_scale_pair(uint32_t byte) {
   constexpr uint32_t kAdd = kFp8 ? 88u : 94u;
-  const uint32_t f = byte + kAdd > 254u ? 0x7FFFu : (byte + kAdd) << 7;
+  const uint32_t f = byte + kAdd <= 254u ? (byte + kAdd) << 7 : (byte == 255u ? 0x7FFFu : 0x7F80u + (byte + kAdd - 254u));
   return f * 0x00010001u;
 }
 // Bits 15..8 of both halves of x hold E4M3 bytes -> their bits as bf16 (2^120 too small).

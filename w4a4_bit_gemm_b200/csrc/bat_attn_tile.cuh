@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
         tmem_ld_32x32b_x32(o_col(t) + lane_base + 32 * b, o);
         tmem_wait_ld();
         float v[32];
-        const float f = part ? attn::kUp : inv;
+        const float f = part ? attn::kUp * 0x1p-40f : inv;
         // (a row that saw nothing: its sums are 0, whatever a NaN in q may have left in them)
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[attn_v_order<kFp8>(j)] = l == 0.0f ? 0.0f : __uint_as_float(o[j]) * f;
@@ -703,8 +703,9 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
       }
       if (valid) {
         if (part) {
-          p.part_ml[2 * prow] = m;
-          p.part_ml[2 * prow + 1] = l;
+          // (against the reference's upper bound: parts then stay as small as the output)
+          p.part_ml[2 * prow] = m + 40.0f;
+          p.part_ml[2 * prow + 1] = l * 0x1p-40f;
         } else if (p.lse) {
           p.lse[tok * p.Hq + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
         }
@@ -789,7 +790,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
           constexpr int kSeq = 2 * kNB;
           const int e = kv * kNB + b;
             uint4(&src)[kBatch] = buf[e & 1];
-          uint32_t nan = 0u;  // some byte's bit 7: a NaN among the batch's V codes
+          uint32_t nan = 0u;  // some byte's bit 7: the batch's V goes the rare way (a NaN code, or its scale)
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             const int tk = 16 * lw + (b * kBatch + k) * kTpi + sub;
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
 #pragma unroll
               for (int q = 0; q < kX; ++q) x[q] = attn_mul_f16x2(x[q], f);
             } else {
-              if (f == 0x7FFF7FFFu) nan = 0x80u;
+              if (f >= 0x7F800000u) nan = 0x80u;  // a NaN or a large scale
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 if (kFp8) {
@@ -824,30 +825,39 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
             put(stage, b * kBatch + k, x);
           }
           if (kv == 1 && (nan & 0x80808080u) != 0u) {
-            // the rare way round: the pieces with a NaN again (from the cache), with 0 in its place,
-            // and a note
+            // the rare way round: pieces with a NaN again (from the cache), with 0 in its place and a note,
+            // and pieces with a scale that takes two steps
 #pragma unroll 1
             for (int k = b * kBatch; k < (b + 1) * kBatch; ++k) {
               const int tk = 16 * lw + k * kTpi + sub;
               const uint32_t f = ix.fac[1][tk][pblk];
-              const bool all = f == 0x7FFF7FFFu;
+              const bool all = f == 0x7FFF7FFFu, large = !all && f >= 0x7F800000u;
+              const uint32_t f1 = large ? 0x7F007F00u : f;
+              const uint32_t f2 = (large ? 127u + (f & 0x7Fu) : 127u) << 7, f22 = f2 << 16 | f2;
               const uint4 v = __ldg(reinterpret_cast<const uint4*>(
                   p.v_codes + piece_off + static_cast<uint64_t>(ix.row[tk]) * static_cast<uint32_t>(row_bytes)));
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
               uint32_t x[kX], any = 0u;
 #pragma unroll
               for (int q = 0; q < kX; ++q) x[q] = 0u;
-              if (kFp8 && !all) {
+              if (!all) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                  const uint32_t z = attn_e4m3_nan(w[q]) & 0x80808080u;
-                  any |= z;
-                  x[2 * q] = attn_mul_bf16x2(attn_e4m3_bits(w[q] << 8), f) &
-                             ((z & 0x80u ? 0u : 0xFFFFu) | (z & 0x800000u ? 0u : 0xFFFF0000u));
-                  x[2 * q + 1] = attn_mul_bf16x2(attn_e4m3_bits(w[q]), f) &
-                                 ((z & 0x8000u ? 0u : 0xFFFFu) | (z & 0x80000000u ? 0u : 0xFFFF0000u));
+                  if (kFp8) {
+                    const uint32_t z = attn_e4m3_nan(w[q]) & 0x80808080u;
+                    any |= z;
+                    x[2 * q] = attn_mul_bf16x2(attn_mul_bf16x2(attn_e4m3_bits(w[q] << 8), f1), f22) &
+                               ((z & 0x80u ? 0u : 0xFFFFu) | (z & 0x800000u ? 0u : 0xFFFF0000u));
+                    x[2 * q + 1] = attn_mul_bf16x2(attn_mul_bf16x2(attn_e4m3_bits(w[q]), f1), f22) &
+                                   ((z & 0x8000u ? 0u : 0xFFFFu) | (z & 0x80000000u ? 0u : 0xFFFF0000u));
+                  } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+                      x[4 * q + h] = attn_mul_bf16x2(attn_mul_bf16x2(attn_e2m1_bits(w[q] << (12 - 4 * h)), f1), f22);
+                  }
                 }
               }
+              if (large) put(stage, k, x);
               if (any != 0u || all) {
                 put(stage, k, x);
                 if (has) {
