@@ -47,7 +47,9 @@ constexpr int kRegsSoftmax = 112, kRegsLoad = 104, kRegsOther = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsOther <= 5 * 96, "the split stays within the launch's registers");
 constexpr int kInfo = 8;                // chunks whose notes are kept
 // A note is overwritten eight chunks on, by a warp that is at most kSlots chunks ahead of the loaders,
-// and they at most kStages / 2 chunks ahead of the products whose softmax read it.
+// and they at most kStages / 2 chunks ahead of the products whose softmax read it. (A unit's last note is read
+// after its last product: by a tile that the next unit has too before its first weights there, by tile 1 where the
+// next unit lacks it before its warps' arrival there, without which that unit gets no q.)
 
 template <int kDP>
 struct Cfg {
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
   __shared__ uint32_t s_nan[C::kRows][kDP / 32];  // written only where a NaN was seen
   __shared__ __align__(16) float s_oa[64];
   __shared__ __align__(16) float s_ob[kDP / 32 * 16];
-  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 2 * 5 + 2 * C::kSlots + 1];
+  __shared__ __align__(8) uint64_t s_bar[2 * kStages + 2 * 5 + 2 * C::kSlots + 2];
   __shared__ uint32_t s_tmem;
   __shared__ AttnPlace s_place;
   __shared__ int64_t s_run;
@@ -371,6 +373,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
   auto i_full = [&](int s) { return bars + 8 * (2 * kStages + 10 + s); };
   auto i_empty = [&](int s) { return bars + 8 * (2 * kStages + 10 + C::kSlots + s); };
   const uint32_t drain = bars + 8 * (2 * kStages + 10 + 2 * C::kSlots);
+  // (the barrier behind it: tile 1's warps have left a unit for one that has no tile 1)
 
   allow_dependents();
   if (threadIdx.x == 0) {
@@ -390,6 +393,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
       mbar_init(i_empty(i), attn_tile::kLoadWarps);
     }
     mbar_init(drain, 1);
+    mbar_init(drain + 8, 4);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 16) {
@@ -429,11 +433,16 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
     const uint32_t lane_base = static_cast<uint32_t>(warp & 3) << 21;  // 32 lanes a warp, bits 16 up
     uint32_t n_s = 0;  // chunks of this tile so far (phases of s_full, o_full)
     uint32_t n_c = 0;  // chunks of the run so far (the notes' ring)
+    uint32_t n_left = 0;  // n_s at the last unit without this tile
     bool ok = t < C::kTiles;
     grid_dependency_wait();  // the q rows' factors
     for (int seg = 0; ok && run.left > 0; ++seg) {
       const int n = run.chunks_here();
       if (t >= run.tiles(p)) {
+        if (n_s != n_left) {
+          if (lane == 0) mbar_arrive(drain + 8);
+          n_left = n_s;
+        }
         run.next_unit(p, n);
         n_c += n;
         continue;
@@ -1070,11 +1079,16 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
       }
     } else {
       // ============================================================== q tiles
-      uint32_t n_q[2] = {0u, 0u};
-      bool ok = true;
+      uint32_t n_q[2] = {0u, 0u}, n_left = 0u;
+      bool ok = true, two = false;
       grid_dependency_wait();  // the q rows
       while (ok && run.left > 0) {
         const int tiles = C::kTiles == 1 ? 1 : run.tiles(p);
+        // (a unit of one tile goes at tile 0's pace, and tile 1's warps may still be reading the unit before's
+        // last note: it gets its q, and so begins, when they have left that unit)
+        if (two && tiles == 1)
+          ok = __all_sync(0xffffffffu, mbar_wait(drain + 8, n_left++ & 1u, kErrWaitEmpty));
+        two = tiles == 2;
         for (int t = 0; ok && t < tiles; ++t) {
           ok = __all_sync(0xffffffffu, mbar_wait(q_free(t), (n_q[t] & 1u) ^ 1u, kErrWaitEmpty));
           if (!ok) break;
