@@ -511,14 +511,18 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
         if (!ok) break;
         tc_fence_after();
         // V of the chunk before is complete: its notes
-        if (i > 0 && (attn_note_any(notes[(n_c - 1) % attn_tile::kInfo]) & kNoteSome)) see_nan(n_c - 1, chunk - 1);
+        if (i > 0 && (attn_note_any(notes[(n_c - 1) % attn_tile::kInfo]) & kNoteSome)) {
+          see_nan(n_c - 1, chunk - 1);
+          __syncwarp();
+        }
         const AttnNote& note = notes[n_c % attn_tile::kInfo];
         // factor of 16 columns (their tokens share a loader warp)
         auto cc = [&](int g) { return fmaxf(cs * note.kfac[g], 1e-37f); };
         const int i0 = chunk * 128;
         // masked columns go to TMEM as -inf, so that the pass below needs no test
         const bool whole = (i0 >= all_lo || i0 + 128 <= sp.ns) && i0 + 128 <= all_hi;
-        const int some = attn_note_any(note);
+        // (one lane's view for the warp: the loaders may be adding to the note)
+        const int some = __shfl_sync(0xffffffffu, attn_note_any(note), 0);
         if (!whole || some) {
           if (some & (kNoteApart | kNoteWide)) {
             const int64_t row = static_cast<int64_t>(run.pl.tile) * kTile + 128 * t + rr;
@@ -632,6 +636,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
       const float inv = l > 0.0f ? attn::kUp / l : (l == 0.0f ? 0.0f : l);
       for (int b = 0; b < p.nb; ++b) {
         uint32_t o[32];
+        __syncwarp();  // (rows that are not there or saw a NaN took another way)
         tmem_ld_32x32b_x32(o_col(t) + lane_base + 32 * b, o);
         tmem_wait_ld();
         float v[32];
