@@ -107,6 +107,7 @@ class Case:
         k_all, v_all = self.K.values(), self.V.values()
         out = torch.zeros(self.T, self.Hq, D, dtype=torch.float64)
         bar, lse = torch.zeros_like(out), torch.full((self.T, self.Hq), -math.inf, dtype=torch.float64)
+        self.lse_bar = torch.zeros_like(lse)
         t0 = l0 = 0
         for n, L in self.seqs:
             pos, j = torch.arange(L - n, L)[:, None], torch.arange(L)[None]
@@ -129,11 +130,13 @@ class Case:
                 o = torch.einsum("tk,tkd->td", p, vv)
                 mag = torch.einsum("tk,tkd->td", p, vv.abs())
                 off = torch.einsum("tk,tkd->td", p * e, vv.abs())
-                big = (p[:, :, None] * vv.abs()).amax((1, 2), keepdim=False)[:, None]
+                big = (p[:, :, None] * vv.abs()).nan_to_num(0.0).amax((1, 2))[:, None]
                 b = mag * (u + 2.0 ** -16) + off + o.abs() * (p * e).sum(1, keepdim=True) + L * (2.0 ** -94 + big * 2.0 ** -110)
                 out[t0:t0 + n, h] = o
                 bar[t0:t0 + n, h] = b * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs()
                 lse[t0:t0 + n, h] = (m + torch.log(z)).squeeze(1)
+                # the scores' errors, and fp32's of the maximum, the sum and the logarithm
+                self.lse_bar[t0:t0 + n, h] = (p * e).sum(1) + 2.0 ** -20 + 2.0 ** -21 * lse[t0:t0 + n, h].abs()
             t0 += n
             l0 += L
         return out, bar, lse
@@ -148,4 +151,7 @@ class Case:
         bad = ~nan & ~(err <= bar)
         assert not bad.any(), (torch.argwhere(bad)[:4].tolist(), int(bad.sum()),
                                float((err / bar)[bad].max()), float((err / ref.abs())[bad].max()))
+        off = (lse.double() - z).abs()
+        assert torch.equal(torch.isnan(lse), torch.isnan(z))
+        assert not (~torch.isnan(z) & ~(off <= self.lse_bar)).any(), float((off / self.lse_bar).nan_to_num(0.0).max())
         return out, lse
