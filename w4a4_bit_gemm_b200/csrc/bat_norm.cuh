@@ -127,6 +127,23 @@ __device__ __forceinline__ void norm_transform(const NormParams& p, float (&y)[1
   }
 }
 
+// (a NaN among the operands stays)
+__device__ __forceinline__ float norm_min(float a, float b, float c) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float norm_max(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 1 / sqrt(sum / K + eps). A sum that fp32 does not hold would give 0, and so codes 0: it makes the row NaN.
+__device__ __forceinline__ float norm_root(const NormParams& p, float sum) {
+  const float r = __frsqrt_rn(__fmaf_rn(sum, p.inv_k, p.eps));
+  return r > 0.0f ? r : NAN;
+}
+
 // Clip, scale and codes of the lane's channels, y = (h w) P without the root `inv`.
 template <bool kFp8>
 __device__ __forceinline__ void norm_quant(const NormParams& p, float (&y)[16], int vec, bool has, int64_t row,
@@ -135,15 +152,17 @@ __device__ __forceinline__ void norm_quant(const NormParams& p, float (&y)[16], 
   float mn = y[0], mx = y[0];
 #pragma unroll
   for (int j = 1; j < 15; j += 2) {
-    asm("min.f32 %0, %0, %1, %2;" : "+f"(mn) : "f"(y[j]), "f"(y[j + 1]));
-    asm("max.f32 %0, %0, %1, %2;" : "+f"(mx) : "f"(y[j]), "f"(y[j + 1]));
+    mn = norm_min(mn, y[j], y[j + 1]);
+    mx = norm_max(mx, y[j], y[j + 1]);
   }
-  mn = fminf(mn, y[15]);
-  mx = fmaxf(mx, y[15]);
+  mn = norm_min(mn, y[15], __shfl_xor_sync(0xffffffffu, norm_min(mn, y[15], y[15]), 1));
+  mx = norm_max(mx, y[15], __shfl_xor_sync(0xffffffffu, norm_max(mx, y[15], y[15]), 1));
   // (rounding is monotonic: the extremes of the rounded products are the rounded extremes)
-  mn = __fmul_rn(fminf(mn, __shfl_xor_sync(0xffffffffu, mn, 1)), inv);
-  mx = __fmul_rn(fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1)), inv);
-  const float lo = __fmul_rn(r_lo, mn), hi = __fmul_rn(r_hi, mx);
+  mn = __fmul_rn(mn, inv);
+  mx = __fmul_rn(mx, inv);
+  // a block with a value that is not finite: scale byte NaN, codes 0 (the clip to [0, 0])
+  const bool bad = !(fabsf(mn) < INFINITY && fabsf(mx) < INFINITY);
+  const float lo = bad ? 0.0f : __fmul_rn(r_lo, mn), hi = bad ? 0.0f : __fmul_rn(r_hi, mx);
   const float amax = fmaxf(fabsf(fminf(fmaxf(mn, lo), hi)), fabsf(fminf(fmaxf(mx, lo), hi)));
   constexpr int kEmax = kFp8 ? 8 : 2;
   const int ef = static_cast<int>(__float_as_uint(amax) >> 23);
@@ -180,7 +199,7 @@ __device__ __forceinline__ void norm_quant(const NormParams& p, float (&y)[16], 
   }
   // the scale bytes of blocks 4g .. 4g+3 are one word of the tiled layout; blocks past nb
   // come from lanes without channels and are the layout's zero padding
-  uint32_t word = static_cast<uint32_t>(sbyte) << (8 * (blk & 3));
+  uint32_t word = static_cast<uint32_t>(has && bad ? 255 : sbyte) << (8 * (blk & 3));
   word |= __shfl_xor_sync(0xffffffffu, word, 2);
   word |= __shfl_xor_sync(0xffffffffu, word, 4);
   if (has && (lane & 7) == 0)
@@ -320,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
         norm_transform<kX>(p, y[i], vec, vec < nvec, sa, bq[i]);
       }
       __syncthreads();
-      const float inv = __frsqrt_rn(__fmaf_rn(norm_sum_get(red[turn]), p.inv_k, p.eps));
+      const float inv = norm_root(p, norm_sum_get(red[turn]));
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const int vec = tid + i * nt;
@@ -343,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
       }
       norm_sum_put(ss, red[turn]);
       __syncthreads();
-      const float inv = __frsqrt_rn(__fmaf_rn(norm_sum_get(red[turn]), p.inv_k, p.eps));
+      const float inv = norm_root(p, norm_sum_get(red[turn]));
       for (int it = 0; it < iters; ++it) {
         const int vec = tid + it * nt;
         const bool has = vec < nvec;
