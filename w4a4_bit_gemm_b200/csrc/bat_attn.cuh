@@ -491,8 +491,8 @@ struct AttnRowCfg {
   static constexpr int kVs = kBytes + 16;
   static constexpr int kStages = !kFp8 && kNB == 2 ? 3 : 2;
   static constexpr int kStageBytes = kTok * (kKs + kVs);
-  // factors of a tile: K scales fp32 [32][kNB], V factors f16 [kNB][32], E fp32 [32], the spread
-  static constexpr int kFacBytes = kTok * kNB * 4 + kTok * kNB * 2 + kTok * 4 + 16;
+  // factors of a tile: K scales fp32 [32][kNB], V factors f16 [kNB][32], E and the least e_b bf16 [32][2]
+  static constexpr int kFacBytes = kTok * kNB * 4 + kTok * kNB * 2 + kTok * 4;
   static constexpr int kWarpBytes = kStages * kStageBytes + 2 * kFacBytes;
 };
 constexpr size_t attn_rows_ring_bytes(int warp_bytes, int nt, int nb) {
@@ -610,29 +610,31 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     // the lane's token's scale bytes, four a word
     constexpr int kW = (kNB + 3) / 4;
     uint32_t sck[kW], scv[kW];
-    auto scale_bytes = [&](const uint8_t* scales, int row, uint32_t (&sc)[kW]) {
-      const uint8_t* src = scales + static_cast<int64_t>(max(row, 0)) * p.nb;
+    auto load_scales = [&](int row) {
+      const int64_t at = static_cast<int64_t>(max(row, 0)) * p.nb;
 #pragma unroll
       for (int w = 0; w < kW; ++w) {
-        sc[w] = 0u;
+        sck[w] = scv[w] = 0u;
         if (row < 0) continue;
         if (p.scale_words) {
-          if (4 * w < p.nb) sc[w] = __ldg(reinterpret_cast<const uint32_t*>(src) + w);
+          if (4 * w < p.nb) {
+            sck[w] = __ldg(reinterpret_cast<const uint32_t*>(p.k_scales + at) + w);
+            scv[w] = __ldg(reinterpret_cast<const uint32_t*>(p.v_scales + at) + w);
+          }
         } else {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (4 * w + k < p.nb) sc[w] |= static_cast<uint32_t>(__ldg(src + 4 * w + k)) << (8 * k);
+            if (4 * w + k < p.nb) {
+              sck[w] |= static_cast<uint32_t>(__ldg(p.k_scales + at + 4 * w + k)) << (8 * k);
+              scv[w] |= static_cast<uint32_t>(__ldg(p.v_scales + at + 4 * w + k)) << (8 * k);
+            }
         }
       }
-    };
-    auto load_scales = [&](int row) {
-      scale_bytes(p.k_scales, row, sck);
-      scale_bytes(p.v_scales, row, scv);
     };
     auto put_scales = [&](int par) {
       float* fk = reinterpret_cast<float*>(facs + par * C::kFacBytes);
       uint16_t* fv = reinterpret_cast<uint16_t*>(fk + C::kTok * kNB);
-      float* fe = reinterpret_cast<float*>(fv + C::kTok * kNB);
+      uint32_t* fe = reinterpret_cast<uint32_t*>(fv + C::kTok * kNB);
       uint32_t nan = 0u;  // a byte 255
 #pragma unroll
       for (int w = 0; w < kW; ++w)
@@ -675,11 +677,8 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
 #pragma unroll
       for (int b = 0; b < kNB; b += 2)
         *reinterpret_cast<float2*>(fk + lane * kNB + b) = make_float2(kf[b], kf[b + 1]);
-      fe[lane] = static_cast<float>(top - 127);
-      // the tile's spread, the largest E - e_b of a token (blocks of scale byte 0, in practice all
-      // zeros, do not count), less the bits below M that f16 has
-      const unsigned spread = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(max(top - 1 - low, 0)));
-      if (lane == 0) fe[C::kTok] = static_cast<float>(static_cast<int>(spread) - 27);
+      // E and the least e_b (blocks of scale byte 0, in practice all zeros, do not count)
+      fe[lane] = attn_pack(static_cast<float>(top - 127), low == 255 ? INFINITY : static_cast<float>(low - 126));
     };
 
     int rw[kS + 1];  // cache rows of tiles i .. i + kS - 1 of the warp, a token a lane
@@ -782,7 +781,7 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
       const uint8_t* vt = kt + C::kTok * C::kKs;
       const float* fk = reinterpret_cast<const float*>(facs + par * C::kFacBytes);
       const uint16_t* fv = reinterpret_cast<const uint16_t*>(fk + C::kTok * kNB);
-      const float* fe = reinterpret_cast<const float*>(fv + C::kTok * kNB);
+      const uint32_t* fe = reinterpret_cast<const uint32_t*>(fv + C::kTok * kNB);
       // ---- S^T = K q^T for the tile's halves of 16 tokens, a block at a time
       float s[2][kNT][4];
 #pragma unroll
@@ -821,41 +820,53 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
       }
       // ---- softmax over the tokens, for the columns 2c and 2c + 1
       const unsigned there = __ballot_sync(0xffffffffu, rw[0] >= 0);
-      float e[2][2];
+      if (there == 0u) {  // (a NaN in q does not count then)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        e[u][0] = fe[16 * u + r];
-        e[u][1] = fe[16 * u + r + 8];
-      }
-      // A normal f16 factor needs x + E - M + 13 - (E - e_b) >= -14. (Tokens that are not there: -inf + inf is
-      // NaN, which the minimum and the maximum pass over.)
-      float el[2][2];
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        el[u][0] = there >> (16 * u + r) & 1u ? e[u][0] : INFINITY;
-        el[u][1] = there >> (16 * u + r + 8) & 1u ? e[u][1] : INFINITY;
+          for (int t = 0; t < kNT; ++t) s[u][t][0] = s[u][t][1] = s[u][t][2] = s[u][t][3] = 0.0f;
       }
-      const float reach = fe[C::kTok];
+      // E, the least e_b (infinite for tokens that are not there), and 0 or -inf
+      float e[2][2], el[2][2], bias[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t w = fe[16 * u + 8 * k + r];
+          e[u][k] = bf16lo(w);
+          el[u][k] = bf16hi(w);
+          bias[u][k] = there >> (16 * u + 8 * k + r) & 1u ? 0.0f : -INFINITY;
+        }
+      // A normal f16 factor needs x + E - M + 13 - (E - e_b) >= -14.
       bool far[kNT][2], wide = false;  // columns that go the wide way; any of the warp's
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
         float top[2], topv[2], low[2];
+        const uint64_t cs2 = pack2(cs[t][0], cs[t][1]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          // tokens r and r + 8 of the half, columns 2c and 2c + 1 side by side
+          float xe[2][2], xl[2][2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float &x0 = s[u][t][k], &x1 = s[u][t][k + 2];
-            x0 = there >> (16 * u + r) & 1u ? x0 * cs[t][k] : -INFINITY;
-            x1 = there >> (16 * u + r + 8) & 1u ? x1 * cs[t][k] : -INFINITY;
-            const float e0 = x0 + el[u][0], e1 = x1 + el[u][1];
-            top[k] = u ? attn_max3(top[k], x0, x1) : fmaxf(x0, x1);
-            topv[k] = u ? attn_max3(topv[k], e0, e1) : fmaxf(e0, e1);
-            low[k] = u ? attn_min3(low[k], e0, e1) : fminf(e0, e1);
+            float &x0 = s[u][t][2 * k], &x1 = s[u][t][2 * k + 1];
+            const uint64_t x = ffma2(pack2(x0, x1), cs2, pack2(bias[u][k], bias[u][k]));
+            unpack2(x, x0, x1);
+            unpack2(fadd2(x, pack2(e[u][k], e[u][k])), xe[k][0], xe[k][1]);
+            unpack2(fadd2(x, pack2(el[u][k], el[u][k])), xl[k][0], xl[k][1]);
           }
+          // (-inf + inf, of a token that is not there, is NaN and passed over)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            top[k] = u ? attn_max3(top[k], s[u][t][k], s[u][t][2 + k]) : fmaxf(s[u][t][k], s[u][t][2 + k]);
+            topv[k] = u ? attn_max3(topv[k], xe[0][k], xe[1][k]) : fmaxf(xe[0][k], xe[1][k]);
+            low[k] = u ? attn_min3(low[k], xl[0][k], xl[1][k]) : fminf(xl[0][k], xl[1][k]);
+          }
+        }
         const bool up = top[0] > m[t][0] + 8.0f || top[1] > m[t][1] + 8.0f || topv[0] > mv[t][0] + 2.0f ||
                         topv[1] > mv[t][1] + 2.0f;
-        far[t][0] = low[0] < mv[t][0] + reach;
-        far[t][1] = low[1] < mv[t][1] + reach;
+        far[t][0] = low[0] < mv[t][0] - 27.0f;
+        far[t][1] = low[1] < mv[t][1] - 27.0f;
         if (__any_sync(0xffffffffu, up || far[t][0] || far[t][1])) {
           if (__any_sync(0xffffffffu, up)) {
             float f[2];
@@ -885,7 +896,7 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
           const unsigned mine = 0x11111111u << c;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const unsigned any = __ballot_sync(0xffffffffu, low[k] < mv[t][k] + reach);
+            const unsigned any = __ballot_sync(0xffffffffu, low[k] < mv[t][k] - 27.0f);
             far[t][k] = (any & mine) != 0u;
             wide |= any != 0u;
           }
@@ -962,7 +973,14 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
       if (__builtin_expect(wide, 0)) {
         // ---- the wide way, for the columns that take it (the others' weights are 0)
         uint32_t mine[kW];  // the token's V scales again
-        scale_bytes(p.v_scales, rw[0], mine);
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+          mine[w] = 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (rw[0] >= 0 && 4 * w + k < p.nb)
+              mine[w] |= static_cast<uint32_t>(__ldg(p.v_scales + static_cast<int64_t>(rw[0]) * p.nb + 4 * w + k)) << (8 * k);
+        }
         int top = 0;
 #pragma unroll
         for (int b = 0; b < kNB; ++b) {
