@@ -8,7 +8,8 @@ Bars, per output channel d of a row, from the arithmetic (p_j the softmax weight
     products, the subtraction of the maximum, the exponential), which changes its weight by a factor
     within exp(+-2 e_j) and the weights' sum in proportion;
   * fp32 sums over the tokens: 2^-16 sum_j p_j |v_jd| covers 2^-24 times a few hundred partial sums;
-  * weights below 2^-126 of the largest weight times scale, and products below 2^-94, may be lost;
+  * weights below 2^-126 of the row's largest (single tokens: times the token's V scale), and products
+    below 2^-94, may be lost;
   * the output is rounded once to bf16: 2^-8 |out|.
 q is bf16 and goes to f16 by a power of two a row, exactly for channels within 2^-28 of the row's
 largest; q below are far inside that.
@@ -120,9 +121,11 @@ class Case:
                 x = (q @ k.T * scale).masked_fill(~see, -math.inf)
                 a = (q.abs() @ k.abs().T * abs(scale)).masked_fill(~see, 0.0)
                 m = x.amax(1, keepdim=True)
+                none = ~see.any(1)  # rows that see nothing: out 0, lse -inf
+                m[none] = 0.0
                 w = torch.exp(x - m)
                 z = w.sum(1, keepdim=True)
-                p = w / z
+                p = torch.where(none[:, None], 0.0, w / z)
                 e = torch.expm1(2 * (a * 2.0 ** -22 * math.sqrt(D) + 2.0 ** -22).clamp(max=300.0))
                 e = torch.where(p > 0, e, 0.0)
                 # (a value that a row does not see takes no part, a NaN neither)
@@ -132,6 +135,9 @@ class Case:
                 off = torch.einsum("tk,tkd->td", p * e, vv.abs())
                 big = (p[:, :, None] * vv.abs()).nan_to_num(0.0).amax((1, 2))[:, None]
                 b = mag * (u + 2.0 ** -16) + off + o.abs() * (p * e).sum(1, keepdim=True) + L * (2.0 ** -94 + big * 2.0 ** -110)
+                if not row_kernel:
+                    lost = torch.where(p < 2.0 ** -126 * p.amax(1, keepdim=True), p, 0.0)
+                    b = b + torch.einsum("tk,tkd->td", lost, vv.abs().nan_to_num(0.0))
                 out[t0:t0 + n, h] = o
                 bar[t0:t0 + n, h] = b * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs()
                 lse[t0:t0 + n, h] = (m + torch.log(z)).squeeze(1)
@@ -151,7 +157,7 @@ class Case:
         bad = ~nan & ~(err <= bar)
         assert not bad.any(), (torch.argwhere(bad)[:4].tolist(), int(bad.sum()),
                                float((err / bar)[bad].max()), float((err / ref.abs())[bad].max()))
-        off = (lse.double() - z).abs()
+        off = torch.where(torch.isneginf(z) & torch.isneginf(lse), 0.0, (lse.double() - z).abs())
         assert torch.equal(torch.isnan(lse), torch.isnan(z))
         assert not (~torch.isnan(z) & ~(off <= self.lse_bar)).any(), float((off / self.lse_bar).nan_to_num(0.0).max())
         return out, lse

@@ -758,11 +758,14 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     put_scales(0);
     load_scales(rw[1]);
 
-    // m, M: running references of the scores and of score + E (within 2^8 and 2^2 of the maxima)
+    // m: running reference of the scores, within 2^8 of the maximum (0 before anything is seen); mv = M - m
+    // with M that of score + E, within 2^2 (-inf before). The scores x below are all relative to m, so that large
+    // ones do not take E's bits.
     float m[kNT][2], mv[kNT][2], l[kNT][2], o[kNT][2 * kNB][4];
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
-      m[t][0] = m[t][1] = mv[t][0] = mv[t][1] = -INFINITY;
+      m[t][0] = m[t][1] = 0.0f;
+      mv[t][0] = mv[t][1] = -INFINITY;
       l[t][0] = l[t][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < 2 * kNB; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.0f;
@@ -837,12 +840,12 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
           el[u][k] = bf16hi(w);
           bias[u][k] = there >> (16 * u + 8 * k + r) & 1u ? 0.0f : -INFINITY;
         }
-      // A normal f16 factor needs x + E - M + 13 - (E - e_b) >= -14.
+      // A normal f16 factor needs x + E - mv + 13 - (E - e_b) >= -14.
       bool far[kNT][2], wide = false;  // columns that go the wide way; any of the warp's
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
         float top[2], topv[2], low[2];
-        const uint64_t cs2 = pack2(cs[t][0], cs[t][1]);
+        const uint64_t cs2 = pack2(cs[t][0], cs[t][1]), m2 = pack2(-m[t][0], -m[t][1]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           // tokens r and r + 8 of the half, columns 2c and 2c + 1 side by side
@@ -850,7 +853,8 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float &x0 = s[u][t][2 * k], &x1 = s[u][t][2 * k + 1];
-            const uint64_t x = ffma2(pack2(x0, x1), cs2, pack2(bias[u][k], bias[u][k]));
+            // (the score is rounded first: the largest one less m is then 0 or exact, however large)
+            const uint64_t x = fadd2(ffma2(pack2(x0, x1), cs2, pack2(bias[u][k], bias[u][k])), m2);
             unpack2(x, x0, x1);
             unpack2(fadd2(x, pack2(e[u][k], e[u][k])), xe[k][0], xe[k][1]);
             unpack2(fadd2(x, pack2(el[u][k], el[u][k])), xl[k][0], xl[k][1]);
@@ -863,8 +867,7 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
             low[k] = u ? attn_min3(low[k], xl[0][k], xl[1][k]) : fminf(xl[0][k], xl[1][k]);
           }
         }
-        const bool up = top[0] > m[t][0] + 8.0f || top[1] > m[t][1] + 8.0f || topv[0] > mv[t][0] + 2.0f ||
-                        topv[1] > mv[t][1] + 2.0f;
+        const bool up = top[0] > 8.0f || top[1] > 8.0f || topv[0] > mv[t][0] + 2.0f || topv[1] > mv[t][1] + 2.0f;
         far[t][0] = low[0] < mv[t][0] - 27.0f;
         far[t][1] = low[1] < mv[t][1] - 27.0f;
         if (__any_sync(0xffffffffu, up || far[t][0] || far[t][1])) {
@@ -872,16 +875,26 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
             float f[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+              const bool first = mv[t][k] == -INFINITY;  // nothing seen yet
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) {
-                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
-                topv[k] = fmaxf(topv[k], __shfl_xor_sync(0xffffffffu, topv[k], d));
-              }
-              top[k] = fmaxf(m[t][k], top[k]);
-              topv[k] = fmaxf(mv[t][k], topv[k]);
-              l[t][k] *= top[k] == -INFINITY ? 1.0f : attn_exp2(m[t][k] - top[k]);
-              f[k] = topv[k] == -INFINITY ? 1.0f : attn_exp2(mv[t][k] - topv[k]);
-              m[t][k] = top[k];
+              for (int d = 4; d < 32; d <<= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], d));
+              top[k] = fmaxf(top[k], first ? -INFINITY : 0.0f);
+              const float mn = top[k] == -INFINITY ? m[t][k] : m[t][k] + top[k], by = mn - m[t][k];
+              m[t][k] = mn;
+              low[k] -= by;
+              topv[k] = -INFINITY;
+#pragma unroll
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  s[u][t][2 * x + k] -= by;
+                  topv[k] = fmaxf(topv[k], s[u][t][2 * x + k] + e[u][x]);
+                }
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) topv[k] = fmaxf(topv[k], __shfl_xor_sync(0xffffffffu, topv[k], d));
+              topv[k] = fmaxf(mv[t][k] - by, topv[k]);
+              l[t][k] *= first ? 1.0f : attn_exp2(-by);
+              f[k] = first ? 1.0f : attn_exp2(mv[t][k] - by - topv[k]);
               mv[t][k] = topv[k];
             }
 #pragma unroll
@@ -936,16 +949,13 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
       uint32_t pb[2][kNT][2];
 #pragma unroll
       for (int t = 0; t < kNT; ++t) {
-        float ms[2], vs[2];
+        float vs[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          ms[k] = m[t][k] == -INFINITY ? 0.0f : m[t][k];
-          vs[k] = far[t][k] ? INFINITY : (mv[t][k] == -INFINITY ? 0.0f : mv[t][k] - 13.0f);
-        }
+        for (int k = 0; k < 2; ++k) vs[k] = far[t][k] ? INFINITY : (mv[t][k] == -INFINITY ? 0.0f : mv[t][k] - 13.0f);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          l[t][0] += attn_exp2(s[u][t][0] - ms[0]) + attn_exp2(s[u][t][2] - ms[0]);
-          l[t][1] += attn_exp2(s[u][t][1] - ms[1]) + attn_exp2(s[u][t][3] - ms[1]);
+          l[t][0] += attn_exp2(s[u][t][0]) + attn_exp2(s[u][t][2]);
+          l[t][1] += attn_exp2(s[u][t][1]) + attn_exp2(s[u][t][3]);
           // weights up to 2^15 in f16 (off by half a step, 2^-11 of each); their sum l keeps fp32
           pb[u][t][0] = attn_transpose8(attn_pack_f16(attn_exp2(s[u][t][0] + (e[u][0] - vs[0])),
                                                       attn_exp2(s[u][t][1] + (e[u][0] - vs[1]))));
@@ -1055,17 +1065,17 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     // ---- join the warps
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
-      float f[2], f2[2];  // 2^(M - 13 - m) in two factors (its exponent may be below fp32's)
+      float f[2], f2[2];  // 2^(mv - 13) in two factors (its exponent may be below fp32's)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
-        const float d = mv[t][k] - 13.0f - m[t][k], d2 = floorf(0.5f * d);
+        const float d = mv[t][k] - 13.0f, d2 = floorf(0.5f * d);
         f[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(d - d2);
         f2[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(d2);
         if (r == 0) {
           float* ml = sml + (warp * kR + 8 * t + 2 * c + k) * 2;
-          ml[0] = m[t][k];
+          ml[0] = mv[t][k] == -INFINITY ? -INFINITY : m[t][k];
           ml[1] = l[t][k];
         }
       }
