@@ -17,7 +17,7 @@ def bat():
 
 
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
-@pytest.mark.parametrize("seqs", [[(1, 300), (1, 70)], [(1, 6000)]])
+@pytest.mark.parametrize("seqs", [[(1, 300), (1, 70)], [(1, 6000)], [(40, 300), (7, 70)]])
 @pytest.mark.parametrize("sign", [1.0, -1.0])
 @pytest.mark.parametrize("size", [8, 14, 18, 22, 28, 34, 50, 80])
 def test_large_scores(bat, fmt, seqs, sign, size):
@@ -54,7 +54,7 @@ def test_large_scores(bat, fmt, seqs, sign, size):
         l0 += L
 
 
-@pytest.mark.parametrize("seqs", [[(1, 300)]])
+@pytest.mark.parametrize("seqs", [[(1, 300)], [(40, 300)]])
 @pytest.mark.parametrize("size", [8, 20, 34, 60])
 def test_equal_large_scores(bat, seqs, size):
     """Two tokens with the same key share the weight."""

@@ -478,6 +478,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
       const int all_lo = p.window > 0 && pos_l - p.window + 1 > sp.lo ? sp.ns + (pos_l - p.window + 1 - sp.lo) : sp.ns;
 
       float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      float thr = -INFINITY;  // a score above it takes the way round: a new reference, or one of a large size
       bool nan_seen = false;  // the row saw a NaN in V; its channels are in s_nan
       auto see_nan = [&](uint32_t c0, int chunk) {
         const AttnNote& nt = notes[c0 % attn_tile::kInfo];
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
         for (int k = 0; k < 4; ++k) {
           uint32_t x[32];
           tmem_ld_32x32b_x32(s_col(t) + lane_base + 32 * k, x);
-          const float c0 = cc(2 * k), c1 = cc(2 * k + 1);
+          float c0 = cc(2 * k), c1 = cc(2 * k + 1);
           attn_tmem_wait(x);
           float mx[2] = {__uint_as_float(x[0]), __uint_as_float(x[16])};
 #pragma unroll
@@ -565,36 +566,48 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
             mx[g] = fmaxf(mx[g], __uint_as_float(x[16 * g + 15]));
           }
           const float top = fmaxf(mx[0] * c0, mx[1] * c1);
-          const bool grow = m == -INFINITY ? top > -INFINITY : top > m + 40.0f;
-          if (__any_sync(0xffffffffu, grow)) {
-            // a new reference, a whole number, so that what is already there is scaled exactly
-            const float mn = grow ? ceilf(top) : m;
-            const float al = m == -INFINITY ? 1.0f : attn_exp2(m - mn);
-            m = mn;
-            l0 *= al;
-            l1 *= al;
-            if (i > 0) {
-              // o of the chunks before: all their MMAs are done
-              ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), (n_s - 1) & 1u, kErrWaitTmemFull)) && ok;
-              tc_fence_after();
+          if (__builtin_expect(__any_sync(0xffffffffu, top > thr), 0)) {
+            const bool grow = m == -INFINITY ? top > -INFINITY : top > m + 40.0f;
+            if (__any_sync(0xffffffffu, grow)) {
+              // a new reference, a whole number, so that what is already there is scaled exactly
+              const float mn = grow ? ceilf(top) : m;
+              const float al = m == -INFINITY ? 1.0f : attn_exp2(m - mn);
+              m = mn;
+              l0 *= al;
+              l1 *= al;
+              if (i > 0) {
+                // o of the chunks before: all their MMAs are done
+                ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), (n_s - 1) & 1u, kErrWaitTmemFull)) && ok;
+                tc_fence_after();
 #pragma unroll 1
-              for (int d = 0; d < p.D; d += 16) {
-                uint32_t o[16];
-                attn_tmem_ld16(o_col(t) + lane_base + d, o);
+                for (int d = 0; d < p.D; d += 16) {
+                  uint32_t o[16];
+                  attn_tmem_ld16(o_col(t) + lane_base + d, o);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
-                tmem_st_32x32b_x16(o_col(t) + lane_base + d, o);
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                  tmem_st_32x32b_x16(o_col(t) + lane_base + d, o);
+                }
+              }
+              tmem_wait_st();
+#pragma unroll 1
+              for (int d = 0; d < 16 * k; d += 16) {
+                uint32_t w[16];
+                attn_tmem_ld16(s_col(t) + lane_base + d, w);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) w[j] = attn_mul_bf16x2(w[j], attn_pack(al, al));
+                tmem_st_32x32b_x16(s_col(t) + lane_base + d, w);
               }
             }
-            tmem_wait_st();
-#pragma unroll 1
-            for (int d = 0; d < 16 * k; d += 16) {
-              uint32_t w[16];
-              attn_tmem_ld16(s_col(t) + lane_base + d, w);
+            // From 2^24 on: below, score times factor less m is not rounded between, and what the rounding of m
+            // left of the largest would no longer be small.
+            const bool large = fabsf(m) >= 0x1p24f && m != -INFINITY;
+            thr = m == -INFINITY || large ? -INFINITY : m + 40.0f;
+            if (large) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = attn_mul_bf16x2(w[j], attn_pack(al, al));
-              tmem_st_32x32b_x16(s_col(t) + lane_base + d, w);
+              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * (j < 16 ? c0 : c1));
+              c0 = c1 = 1.0f;
             }
+            __syncwarp();
           }
           const float ms = m == -INFINITY ? 0.0f : m;
           const uint64_t m2 = pack2(-ms, -ms);
