@@ -368,10 +368,10 @@ typedef struct {
  *              its contents unused after the call. Calls that may overlap on the GPU need
  *              one each.
  * Arithmetic: stored values are used exactly; a scale byte 255 or an E4M3 NaN counts as NaN for
- * the rows that see it. Sums of values of V above 2^100 may overflow. In chunks (see max_q_len) a
- * product of a weight and a value below 2^-94 may count as 0; in single tokens a weight below 2^-126
- * of the largest (weight times the token's largest V scale); in both blocks of scale byte 0
- * (values below 2^-118) may. q P_q is rounded to 11 significant bits (channels below 2^-28 of the row's
+ * the rows that see it. Sums of values of V above 2^100 may overflow. A softmax weight below 2^-126 of
+ * the row's largest (single tokens: weight times the token's largest V scale), in chunks a product
+ * of a weight and a value below 2^-94, and a block of scale byte 0 (values below 2^-118) may
+ * count as 0. q P_q is rounded to 11 significant bits (channels below 2^-28 of the row's
  * largest to 2^-40 of that), each softmax weight, whatever its size, to 11 (single tokens) or 8
  * (chunks) for the products; scores, maxima, sums and outputs are held in fp32 and out is rounded
  * once. Sums run in a fixed order: results do not depend on timing.

@@ -168,3 +168,14 @@ def test_v_scales_above_the_usual(bat, fmt, seqs, by):
     c = Case(bat, seqs, 4, 2, 64, fmt, seed=11)
     c.V.shift((slice(2, None, 5), 1, 1), by)
     c.check()
+
+
+@FMT
+@pytest.mark.parametrize("apart", range(13, 32))
+def test_v_block_far_below_in_the_largest_token(bat, fmt, apart):
+    """Blocks far below in the one token that sets the weights' reference, the others' scales around its least."""
+    c = Case(bat, [(1, 200), (1, 9)], 4, 2, 96, fmt, seed=apart)
+    c.V.shift((5, slice(None), 1), apart)
+    c.V.shift((204, 0, 2), apart)
+    c.check(scale=0.0)
+    c.check()

@@ -677,8 +677,10 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
 #pragma unroll
       for (int b = 0; b < kNB; b += 2)
         *reinterpret_cast<float2*>(fk + lane * kNB + b) = make_float2(kf[b], kf[b + 1]);
-      // E and the least e_b (blocks of scale byte 0, in practice all zeros, do not count)
-      fe[lane] = attn_pack(static_cast<float>(top - 127), low == 255 ? INFINITY : static_cast<float>(low - 126));
+      // E and the least e_b (blocks of scale byte 0, in practice all zeros, do not count; -inf where f16 does not
+      // hold 2^(e_b - E))
+      const float least = low == 255 ? INFINITY : (top - 1 - low > 24 ? -INFINITY : static_cast<float>(low - 126));
+      fe[lane] = attn_pack(static_cast<float>(top - 127), least);
     };
 
     int rw[kS + 1];  // cache rows of tiles i .. i + kS - 1 of the warp, a token a lane
