@@ -8,7 +8,7 @@ Bars, per output channel d of a row, from the arithmetic (p_j the softmax weight
     products, the subtraction of the maximum, the exponential), which changes its weight by a factor
     within exp(+-2 e_j) and the weights' sum in proportion;
   * fp32 sums over the tokens: 2^-16 sum_j p_j |v_jd| covers 2^-24 times a few hundred partial sums;
-  * weights below 2^-126 of the row's largest (single tokens: times the token's V scale), and products
+  * weights below 2^-110 of the row's largest (single tokens: times the token's V scale), and products
     below 2^-94, may be lost;
   * the output is rounded once to bf16: 2^-8 |out|.
 q is bf16 and goes to f16 by a power of two a row, exactly for channels within 2^-28 of the row's
@@ -136,7 +136,7 @@ class Case:
                 big = (p[:, :, None] * vv.abs()).nan_to_num(0.0).amax((1, 2))[:, None]
                 b = mag * (u + 2.0 ** -16) + off + o.abs() * (p * e).sum(1, keepdim=True) + L * (2.0 ** -94 + big * 2.0 ** -110)
                 if not row_kernel:
-                    lost = torch.where(p < 2.0 ** -126 * p.amax(1, keepdim=True), p, 0.0)
+                    lost = torch.where(p < 2.0 ** -110 * p.amax(1, keepdim=True), p, 0.0)
                     b = b + torch.einsum("tk,tkd->td", lost, vv.abs().nan_to_num(0.0))
                 out[t0:t0 + n, h] = o
                 bar[t0:t0 + n, h] = b * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs()

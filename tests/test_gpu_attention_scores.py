@@ -69,3 +69,30 @@ def test_equal_large_scores(bat, seqs, size):
     want = ((v[5] + v[201]) / 2).repeat_interleave(2, 0)[None]
     mag = ((v[5].abs() + v[201].abs()) / 2).repeat_interleave(2, 0)[None]
     assert torch.all((out.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -8 * mag)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+@pytest.mark.parametrize("seqs", [[(1, 300)], [(1, 6000)], [(40, 300)], [(100, 6000)]])
+@pytest.mark.parametrize("steps", [(46, 95), (47, 100), (60, 100), (39, 39)])
+def test_weights_that_wait_for_a_larger_one(bat, fmt, seqs, steps):
+    """Scores that rise in steps from token to token: the weights of before are scaled down by far and still count
+    where the largest one's value is zero."""
+    n, L = seqs[0]
+    first = L - n
+    c = Case(bat, seqs, 2, 1, 64, fmt, seed=4, q=torch.ones(n, 2, 64))
+    one, big = (0x38, 0x40) if fmt == "mxfp8" else (2, 4)  # 1 and 2
+    c.K.codes[:] = 0
+    c.K.scales[:] = 127
+    # 64 channels of 1 times 1 / 8: a key of one block's first channels gives the score; log2 units: / ln 2
+    at = [first // 4, first // 256 * 128 + 100, first - 1]  # (the second behind others of its chunk)
+    score = [-8.0, -8.0 + steps[0], -8.0 + steps[0] + steps[1]]
+    for j, s in zip(at, score):
+        want = round(s * 0.6931 * 8)  # sum of the key's channels
+        size = abs(want) // 64 + 1
+        e = max(0, size.bit_length())
+        c.K.codes[j, 0] = one | ((0x80 if fmt == "mxfp8" else 8) if want < 0 else 0)
+        c.K.codes[j, 0, abs(want) * 64 // (64 * 2 ** e):] = 0
+        c.K.scales[j] = 127 + e
+    c.V.codes[at[2], 0, 20:] = 0
+    c.V.shift(at[1], 50)
+    c.check()

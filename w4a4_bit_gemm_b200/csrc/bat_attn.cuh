@@ -295,6 +295,12 @@ __device__ __forceinline__ float attn_min3(float a, float b, float c) {
   return r;
 }
 
+// 2^d as the product of two numbers, for what is larger than its reference and so may outlast fp32's least 2^d.
+__device__ __forceinline__ float2 attn_exp2_two(float d) {
+  const float h = floorf(0.5f * d);
+  return make_float2(attn_exp2(h), attn_exp2(d - h));
+}
+
 // ---------------------------------------------------------------- stored elements -> f16, bf16
 // f16 takes two codes from one conversion instruction, exactly, and gives q P_q and the weights 11
 // significant bits instead of bf16's 8. Its narrow range is no limit where both sides of a sum
@@ -1067,14 +1073,12 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     // ---- join the warps
 #pragma unroll
     for (int t = 0; t < kNT; ++t) {
-      float f[2], f2[2];  // 2^(mv - 13) in two factors (its exponent may be below fp32's)
+      float2 f[2];  // 2^(mv - 13)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[t][k] += __shfl_xor_sync(0xffffffffu, l[t][k], d);
-        const float d = mv[t][k] - 13.0f, d2 = floorf(0.5f * d);
-        f[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(d - d2);
-        f2[k] = mv[t][k] == -INFINITY ? 0.0f : attn_exp2(d2);
+        f[k] = mv[t][k] == -INFINITY ? make_float2(0.0f, 0.0f) : attn_exp2_two(mv[t][k] - 13.0f);
         if (r == 0) {
           float* ml = sml + (warp * kR + 8 * t + 2 * c + k) * 2;
           ml[0] = mv[t][k] == -INFINITY ? -INFINITY : m[t][k];
@@ -1086,8 +1090,8 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
         // rows r and r + 8 of m-tile i are channels 32 (i / 2) + 4 r + 2 (i % 2) and the next
         const int d = 32 * (i >> 1) + 4 * r + 2 * (i & 1);
         float* o0 = so + (warp * kR + 8 * t + 2 * c) * kLdo + d;
-        *reinterpret_cast<float2*>(o0) = make_float2(o[t][i][0] * f[0] * f2[0], o[t][i][2] * f[0] * f2[0]);
-        *reinterpret_cast<float2*>(o0 + kLdo) = make_float2(o[t][i][1] * f[1] * f2[1], o[t][i][3] * f[1] * f2[1]);
+        *reinterpret_cast<float2*>(o0) = make_float2(o[t][i][0] * f[0].x * f[0].y, o[t][i][2] * f[0].x * f[0].y);
+        *reinterpret_cast<float2*>(o0 + kLdo) = make_float2(o[t][i][1] * f[1].x * f[1].y, o[t][i][3] * f[1].x * f[1].y);
       }
     }
     __syncthreads();
@@ -1099,23 +1103,24 @@ __global__ void __launch_bounds__(attn::kThreads, attn_rows_per_sm(kFp8, kNB, kN
     const int quads = p.D >> 2;
     for (int i = threadIdx.x; i < nrows * quads; i += attn::kThreads) {
       const int n = i / quads, d = 4 * (i - n * quads);
-      float mm = -INFINITY, f[attn::kWarps], sum = 0.0f;
+      float mm = -INFINITY, sum = 0.0f;
+      float2 f[attn::kWarps];
 #pragma unroll
       for (int w = 0; w < attn::kWarps; ++w) mm = fmaxf(mm, sml[(w * kR + n) * 2]);
 #pragma unroll
       for (int w = 0; w < attn::kWarps; ++w) {
         const float2 ml = *reinterpret_cast<const float2*>(sml + (w * kR + n) * 2);
-        f[w] = ml.x == -INFINITY ? 0.0f : attn_exp2(ml.x - mm);
-        sum = ml.y != ml.y ? NAN : __fmaf_rn(ml.y, f[w], sum);  // (a NaN stays: NaN * f + anything)
+        f[w] = ml.x == -INFINITY ? make_float2(0.0f, 0.0f) : attn_exp2_two(ml.x - mm);
+        sum = ml.y != ml.y ? NAN : __fmaf_rn(ml.y * f[w].x, f[w].y, sum);  // (a NaN stays: NaN * f + anything)
       }
       float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < attn::kWarps; ++w) {
         const float4 v = *reinterpret_cast<const float4*>(so + (w * kR + n) * kLdo + d);
-        acc.x = __fmaf_rn(v.x, f[w], acc.x);
-        acc.y = __fmaf_rn(v.y, f[w], acc.y);
-        acc.z = __fmaf_rn(v.z, f[w], acc.z);
-        acc.w = __fmaf_rn(v.w, f[w], acc.w);
+        acc.x = __fmaf_rn(v.x * f[w].x, f[w].y, acc.x);
+        acc.y = __fmaf_rn(v.y * f[w].x, f[w].y, acc.y);
+        acc.z = __fmaf_rn(v.z * f[w].x, f[w].y, acc.z);
+        acc.w = __fmaf_rn(v.w * f[w].x, f[w].y, acc.w);
       }
       if (whole) {
         const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
@@ -1221,16 +1226,17 @@ __global__ void __launch_bounds__(256) bat_attn_join_kernel(const AttnParams p) 
         bad[k] |= ml[k].y != ml[k].y;
         if (ml[k].x == -INFINITY) continue;  // saw nothing
         const float mn = fmaxf(mm[k], ml[k].x);
-        const float f0 = attn_exp2(mm[k] - mn), f1 = attn_exp2(ml[k].x - mn);
+        const float2 f0 = mm[k] == -INFINITY ? make_float2(0.0f, 0.0f) : attn_exp2_two(mm[k] - mn);
+        const float2 f1 = attn_exp2_two(ml[k].x - mn);
         mm[k] = mn;
-        sum[k] = sum[k] * f0 + ml[k].y * f1;
+        sum[k] = sum[k] * f0.x * f0.y + ml[k].y * f1.x * f1.y;
 #pragma unroll
         for (int g = 0; g < 2; ++g)
           if (lane + 32 * g < quads) {
-            acc[k][g].x = acc[k][g].x * f0 + v[k][g].x * f1;
-            acc[k][g].y = acc[k][g].y * f0 + v[k][g].y * f1;
-            acc[k][g].z = acc[k][g].z * f0 + v[k][g].z * f1;
-            acc[k][g].w = acc[k][g].w * f0 + v[k][g].w * f1;
+            acc[k][g].x = acc[k][g].x * f0.x * f0.y + v[k][g].x * f1.x * f1.y;
+            acc[k][g].y = acc[k][g].y * f0.x * f0.y + v[k][g].y * f1.x * f1.y;
+            acc[k][g].z = acc[k][g].z * f0.x * f0.y + v[k][g].z * f1.x * f1.y;
+            acc[k][g].w = acc[k][g].w * f0.x * f0.y + v[k][g].w * f1.x * f1.y;
           }
       }
     }

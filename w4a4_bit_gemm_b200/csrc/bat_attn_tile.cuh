@@ -571,10 +571,10 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
             if (__any_sync(0xffffffffu, grow)) {
               // a new reference, a whole number, so that what is already there is scaled exactly
               const float mn = grow ? ceilf(top) : m;
-              const float al = m == -INFINITY ? 1.0f : attn_exp2(m - mn);
+              const float2 al = m == -INFINITY ? make_float2(1.0f, 1.0f) : attn_exp2_two(m - mn);
               m = mn;
-              l0 *= al;
-              l1 *= al;
+              l0 *= al.x * al.y;
+              l1 *= al.x * al.y;
               if (i > 0) {
                 // o of the chunks before: all their MMAs are done
                 ok = __all_sync(0xffffffffu, mbar_wait(o_full(t), (n_s - 1) & 1u, kErrWaitTmemFull)) && ok;
@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
                   uint32_t o[16];
                   attn_tmem_ld16(o_col(t) + lane_base + d, o);
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al.x * al.y);
                   tmem_st_32x32b_x16(o_col(t) + lane_base + d, o);
                 }
               }
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(attn_tile::kThreads, 1) bat_attn_tile_kernel(
                 uint32_t w[16];
                 attn_tmem_ld16(s_col(t) + lane_base + d, w);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) w[j] = attn_mul_bf16x2(w[j], attn_pack(al, al));
+                for (int j = 0; j < 16; ++j) w[j] = attn_mul_bf16x2(attn_mul_bf16x2(w[j], attn_pack(al.x, al.x)), attn_pack(al.y, al.y));
                 tmem_st_32x32b_x16(s_col(t) + lane_base + d, w);
               }
             }
