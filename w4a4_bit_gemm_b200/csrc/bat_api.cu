@@ -685,15 +685,22 @@ size_t attn_part_bytes(int64_t ctas, int64_t rows, int64_t D) {
 
 // Which kernel. The row kernel reads the cache once for every new token, the tile kernel once for
 // 256 rows, but the latter's fixed time is longer and a tile costs the same for few rows. Measured
-// (B200, KV8, us, row / tile kernel): 32 / 8 heads of 128: 8 sequences x 16384 tokens: 2 new tokens
-// 149 / 209, 4: 262 / 209, 8: 501 / 211; 8 x 2000: 2: 39 / 52, 4: 55 / 52, 8: 90 / 53; 1 x 2000: 8:
-// 32 / 40, 16: 39 / 41, 32: 55 / 45. 28 / 4 heads of 64: 8 x 16384: 4: 93 / 106, 8: 157 / 107; 8 x 2000: 8:
-// 39 / 43, 16: 59 / 45. So: from 4 (6 for narrow heads) new tokens on, if the row kernel's reads, at
-// most new tokens x KV heads x cached tokens x channels as far as the host knows, are worth it.
+// (B200, us, row / tile kernel in a replayed graph with the L2 flushed, KV8; KV4 in brackets; n new tokens a
+// sequence):
+//   heads       8 x 16384 tokens            8 x 2000                                  1 x 2000
+//   32/8, 128   n 4: 287/227 (184/223)      n 4: 60/71 (47/68), 8: 96/72 (70/70)      n 16: 43/56 (39/55)
+//   8/8, 128    n 4: 285/225 (182/223)      n 4: 59/70 (47/68), 8: 94/70 (68/68)      n 16: 41/55 (37/53)
+//   128/8, 128  n 4: 340/231 (285/229)      n 4: 79/74 (70/72), 8: 125/72 (107/70)    n 16: 55/66 (53/66)
+//   28/4, 64    n 4: 104/136, 8: 186/137    n 8: 43/57 (39/57), 16: 63/59 (57/59)     n 16: 33/55 (31/55)
+//   16/8, 256   n 4: 616/344 (348/395)      n 4: 121/88 (76/88)                       n 16: 72/63 (55/61)
+// The group's size hardly matters, the format by a factor of up to 1.6. So: from 4 (6 for narrow heads) new tokens
+// on, if the row kernel's reads, at most new tokens x KV heads x the table's capacity x channels as far as the
+// host knows the lengths, are worth it. (A table with room for far more than is cached, or a window, makes that bound
+// a loose one, and the tile kernel is then taken early.)
 int64_t attn_tile_tokens(int64_t D) { return D > 64 ? 4 : 6; }
 bool attn_use_tile(int64_t T, int64_t H, int64_t D, int64_t capacity, int64_t max_q_len) {
   return max_q_len >= attn_tile_tokens(D) &&
-         static_cast<double>(T * H) * static_cast<double>(capacity) * static_cast<double>(D) >= 48e6;
+         static_cast<double>(T * H) * static_cast<double>(capacity) * static_cast<double>(D) >= 96e6;
 }
 constexpr int kAttnTileCtas = 160;
 int64_t attn_tile_rows(int64_t D) { return D <= 128 ? 256 : 128; }
