@@ -484,9 +484,10 @@ __device__ __forceinline__ void attn_block_apply(const AttnFactors& f, int blk, 
 // within 2^27 of M for blocks of one size), which keeps the weights' 11 bits. A tile where one is not, be it a
 // weight far below the maximum or a block far below its token's largest, takes the wide way: the
 // weights as the sum of two bf16 numbers (16 bits, fp32's range), twice the products.
-// Bound: latency for KV8 (two warps a scheduler; 3.4 to 3.9 TB/s of the measured 6.5), the instructions for
-// KV4 (846 a warp and tile): 8 x 65536 tokens of 8 heads of 128 in 224 us (2.5 TB/s). A step of 16
-// sequences of up to 4096 tokens: 40 us, 8 of them a unit's start (look-ups, q, first copies).
+// Bound: latency for KV8 (two warps a scheduler; 3.3 to 3.8 TB/s of the measured 6.5), the instructions for
+// KV4 (908 a warp and tile): 8 x 65536 tokens of 8 heads of 128 in 227 us (2.5 TB/s). A step of 16
+// sequences of up to 4096 tokens: 42 us, 8 of them a unit's start (look-ups, q, first copies). Where every tile
+// takes the wide way: 8 x 16384 tokens 135 instead of 104 us in KV8, 116 instead of 80 in KV4.
 template <bool kFp8, int kNB>
 struct AttnRowCfg {
   static constexpr int kTok = 32;                            // tokens of a warp's tile

@@ -25,10 +25,13 @@
 // and a 2048-token chunk over 16384 ran 801 us instead of 717. The weights' sum as the test of the
 // reference instead of the maximum: 758 us. An issuing warp for each tile: 848 us, the tiles' MMAs then
 // cut into each other. Without any softmax, stores or loads the MMAs and their hand-offs alone take 535.)
+// (Those figures are from before the paths for keys far apart and for large scores, which cost 3 %.)
 // What bounds it: latency along a chunk's chain (scores, softmax, P V, next scores), with the tensor pipe
-// and the exponentials' unit each about 31 % busy. 2048 new tokens over 16384 (32 / 8 heads of 128, KV8):
-// 707 us, 728 TFLOP/s, 0.44 of a cuBLAS bf16 product's rate; about 5900 cycles a chunk of 256 rows where
+// and the exponentials' unit each about 30 % busy. 2048 new tokens over 16384 (32 / 8 heads of 128, KV8):
+// 729 us, 707 TFLOP/s, 0.43 of a cuBLAS bf16 product's rate; about 6000 cycles a chunk of 256 rows where
 // MMAs and exponentials at their nominal rates would take 2048 each.
+// Weights are bf16 (8 bits) because V is: the two operands of an MMA have one type, and f16 does not hold
+// V's scales. Each is rounded to nearest, so that their errors average out; the sum keeps fp32.
 //
 // A NaN in V must not reach rows that do not see its token, but 0 times NaN in the MMA would
 // carry it there: the loader stores 0 in its place and notes (token, block);

@@ -18,7 +18,9 @@
 // shared memory, one address for the whole warp, each used for both rows); B_b^T (X_r A) takes the
 // other lane's two rows by 16 shuffles. 12 multiply-adds an element instead of the 32 of the
 // 32 x 32 block matrix. (8 channels a lane, a quad a block: 332 instead of 219 instructions for
-// 8 channels; 16384 x 4096 took 132 us.) 16384 x 4096 in MXFP8: 99 us, 4.8 TB/s.
+// 8 channels; 16384 x 4096 took 132 us.) 16384 x 4096 in MXFP8: 102 us, 4.6 TB/s.
+// Other splits (kX 2) form each coefficient from A and B as it comes and spill (up to 6 KB a thread for rows of 8192 to
+// 16384 channels): right, but 16384 x 4096 takes 4.1 ms (1.0 with s = 16).
 // The transform is linear and the norm's root a factor of the whole row, so the transform runs
 // on h w while the row's sum is still on its way through the barrier, and the root is multiplied
 // in afterwards. A row stays in registers, and the next row of the CTA is requested before that
@@ -269,7 +271,7 @@ __device__ __forceinline__ void norm_weight(const uint4 (&wv)[2], float (&h)[16]
 // kV > 0: the row's kV vectors of 16 a thread stay in registers (kV * 16 * blockDim.x >= K).
 // kV == 0: any K, the row is read once for the sum and once for the codes.
 // kThreads: the most threads a CTA is launched with; up to 256, two CTAs share an SM (three, at
-// 80 registers a thread, spill: 16384 x 4096 in 109 instead of 100 us).
+// 80 registers a thread, spill: 16384 x 4096 in 109 us when two took 100).
 template <int kV, int kX, bool kFp8, int kThreads>
 __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1)
     bat_rmsnorm_quantize_kernel(const NormParams p) {
