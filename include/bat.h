@@ -410,8 +410,8 @@ BAT_API bat_status_t bat_kv_attention(const void* q, int64_t T, int64_t Hq, int6
  *   y_out    : optional fp32 [M][K] trace of the transformed values (NULL to skip).
  * A block of y that holds a value that is not finite gets the scale byte 255 (NaN) and codes 0; a
  * product with it gives NaN for its row. A row with a NaN or an infinity, or whose sum of squares is
- * beyond fp32 (|h| of about 1e19), is NaN as a whole, and so is with eps 0 a row of zeros or of |h|
- * below about 1e-22.
+ * beyond fp32 (|h| of about 1.8e19 / sqrt(K)), is NaN as a whole, and so is with eps 0 a row of zeros
+ * or of |h| below about 1e-22.
  * All pointers 16-byte aligned (g_lo, g_hi: 4). Errors: BAT_ERR_UNSUPPORTED (the split),
  * BAT_ERR_INVALID_ARG (null pointers, one of a pair only, M < 1, K < 32, eps, fmt),
  * BAT_ERR_SHAPE, BAT_ERR_ALIGN, BAT_ERR_CUDA, as in bat_quantize_act_gpk.
